@@ -453,6 +453,112 @@ MOE_API int moe_combine(const void *rows, int n_rows, const int32_t *slot_row,
                         const float *shared, int T, int d, int k, int out_dt, void *y,
                         void *status_ws, void *stream);
 
+/*
+ * ---- 8-bit rows, weights and products -------------------------------------
+ *
+ * Codes are e4m3 (one byte; largest value 448, no infinities), with one fp32
+ * scale per block: of 1 x 128 along a row (activations) or of 128 x 128
+ * (weights); the last block of a row or column may be shorter.  A block with
+ * largest magnitude A' has, with A = max(A', 2^-100),
+ *   scale = A / 448 (rounded to fp32),  code = e4m3 nearest to 448 x / A
+ * (ties to even, the quotient taken exactly), so that code * scale is x to
+ * within half a step of e4m3 (2^-4 of the value, or 2^-10 of the scale below
+ * the smallest normal code).  A block with an infinity or a NaN gets a NaN
+ * scale and NaN codes.  Inside a row the scales of its blocks lie rows apart:
+ * scales[block][row], what a tile of rows reads at once is contiguous.
+ *
+ * moe_quantize_rows -- rows in 8 bits.
+ *   x       device, in_dt [R, d] (MOE_BF16 or MOE_F32), d % 16 == 0,
+ *           d <= 196608
+ *   q       device, e4m3 [R, d] out, 16-byte aligned
+ *   scales  device, f32 [ceil(d / 128), R] out
+ * R = 0 queues nothing.  Other sizes: MOE_ERR_UNSUPPORTED.
+ */
+MOE_API int moe_quantize_rows(const void *x, int R, int d, int in_dt, void *q, float *scales,
+                              void *stream);
+
+/*
+ * moe_swiglu_quantize_rows -- h = silu(gate) * up of each row (computed in
+ * fp32), in 8 bits.
+ *   gate_up  device, bf16 [R, 2*inter]: gate, then up; inter % 16 == 0
+ *   w        device, f32 [R], or NULL: each row's scales are multiplied by
+ *            w[r] (a gate weight: the product of the row is w[r] times larger)
+ *   q        device, e4m3 [R, inter] out;  scales  f32 [ceil(inter / 128), R]
+ */
+MOE_API int moe_swiglu_quantize_rows(const void *gate_up, const float *w, int R, int inter,
+                                     int in_dt, void *q, float *scales, void *stream);
+
+/*
+ * moe_quantize_weight -- G weight matrices in 8 bits.
+ *   W       device, in_dt [G, n, k], k % 16 == 0
+ *   q       device, e4m3 [G, n, k] out
+ *   scales  device, f32 [G, ceil(n / 128), ceil(k / 128)] out
+ */
+MOE_API int moe_quantize_weight(const void *W, int G, int n, int k, int in_dt, void *q,
+                                float *scales, void *stream);
+
+/*
+ * moe_matmul_fp8 -- y[r] = sum_k a[r, k] b[g(r), :, k], 8-bit operands with
+ * their block scales, by groups of consecutive rows:
+ *   y[r, n] = sum_j a_scales[j, r] b_scales[g, n / 128, j] *
+ *             sum_{k in block j} a[r, k] b[g, n, k]
+ * The sum inside a block is the tensor core's, the sum over blocks fp32, y is
+ * rounded once.
+ *   a         device, e4m3 [R, k], k % 16 == 0
+ *   a_scales  device, f32 [ceil(k / 128), R]
+ *   b         device, e4m3 [G, n, k]
+ *   b_scales  device, f32 [G, ceil(n / 128), ceil(k / 128)]
+ *   counts    device, int32 [G]: rows of each group (group 0's rows come
+ *             first); rows behind the last group are left as they were.
+ *             Negative counts are taken as 0; counts that add up to more than
+ *             R compute the rows that there are and set MOE_ERR_DEVICE.  NULL:
+ *             G == 1 and all R rows
+ *   y         device, out_dt [R, n] out (MOE_BF16 or MOE_F32)
+ *   status_ws device workspace (256 bytes, 256-byte aligned) whose status
+ *             word receives MOE_ERR_DEVICE or MOE_ERR_TIMEOUT, or NULL.  It is
+ *             not reset by the call (moe_clear_device_status does)
+ * Limits: 1 <= G <= 256.  R = 0 queues nothing.
+ */
+MOE_API int moe_matmul_fp8(const void *a, const float *a_scales, const void *b,
+                           const float *b_scales, const int32_t *counts, int R, int G, int n,
+                           int k, int out_dt, void *y, void *status_ws, void *stream);
+
+/*
+ * ---- The layer for a few tokens -------------------------------------------
+ *
+ * moe_few_max_tokens -- the most tokens moe_forward_few takes for a layer of
+ * these sizes (16, 8, or 0: not at all).  Host only.
+ * moe_few_workspace_bytes -- its workspace (0 for sizes it does not take).
+ */
+MOE_API int moe_few_max_tokens(int d, int E, int k, int inter, int n_shared);
+MOE_API size_t moe_few_workspace_bytes(int T, int d, int E, int k, int inter, int n_shared);
+
+/*
+ * moe_forward_few -- moe_forward_ex for a few tokens, as one stream over the
+ * weights of the touched experts (two launches).  bf16 x and router; the
+ * expert weights are bf16 or, with scales, e4m3 in the same layouts:
+ *   s_gate_up  device, f32 [E, 2*inter/128, d/128]
+ *   s_down     device, f32 [E, d/128, inter/128]
+ *   s_shared   device, f32 [2*S*inter/128, d/128] followed by
+ *              [d/128, S*inter/128]; NULL iff n_shared == 0
+ *   (all NULL: bf16 weights.  moe_quantize_weight makes them.)
+ * h is rounded once to bf16, all sums are fp32 and y is rounded once: the
+ * experts' outputs are not rounded on their own as in moe_forward.  Sums run
+ * in a fixed order: results are bitwise reproducible.  Other arguments as
+ * moe_forward_ex.  Limits: d % 256 == 0, inter % 128 == 0, n_shared <= 64,
+ * T <= moe_few_max_tokens(...) (else MOE_ERR_UNSUPPORTED).  The workspace
+ * needs no initialisation; its first 256 bytes are the status word
+ * (moe_get_device_status).  Calls that overlap in time need workspaces of
+ * their own.  Capturable in a CUDA graph.
+ */
+MOE_API int moe_forward_few(const void *x, const void *W_router, const void *W_gate_up,
+                            const void *W_down, const void *W_shared, const float *s_gate_up,
+                            const float *s_down, const float *s_shared, int T, int d, int E,
+                            int k, int n_group, int topk_group, int inter, int n_shared,
+                            int in_dt, int out_dt, int gate, const float *expert_bias, void *y,
+                            int32_t *topk_idx_out, float *topk_w_out, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* moe_status_string -- static text for a status code. */
 MOE_API const char *moe_status_string(int status);
 

@@ -1,0 +1,478 @@
+// 8-bit product of rows and weights by groups of rows (experts):
+//
+//   y[r, n] = sum_j sa[j, r] sb[g, n / 128, j] P_j[r, n],
+//   P_j[r, n] = sum_{k in block j} a[r, k] b[g, n, k]      (e4m3 operands)
+//
+// P_j is a tcgen05 product (kind::f8f6f4, fp32 accumulator in TMEM) of one
+// 128-deep block.  The scales are arbitrary fp32 numbers, so they cannot ride
+// in the tensor core's own block scaling: the epilogue warps take P_j out of
+// TMEM and add it, scaled, to fp32 sums in registers, block by block, while
+// the tensor core makes the next block in the other half of TMEM.  The rows
+// are the M side of the product: a thread owns one row of the tile, so its
+// scale is one register, and b's scale is one number for 128 columns.
+//
+// CTA (one per SM, persistent): 128 rows x BN columns.  Warp 0 loads the
+// operands by TMA (128-byte swizzle) into a ring of stages, warp 1 issues the
+// products, warps 4..11 add (two warps per SM sub-partition: TMEM lanes
+// 32 (w % 4).., columns half (w - 4) / 4).  128 sums a thread need more
+// registers than an even split leaves: warps 0..3 hand theirs over (of the
+// launch's 384 x 168, 128 x 56 + 256 x 224).
+#include <cudaTypedefs.h>
+#include <limits.h>
+
+#include <algorithm>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kM8 = 128;          // rows of a tile
+constexpr int kK8 = 128;          // depth of a block
+constexpr int kEpiWarps8 = 8;
+constexpr int kThreads8 = 32 * (4 + kEpiWarps8);
+constexpr int kABytes8 = kM8 * kK8;
+constexpr uint64_t kDrainNs8 = 1000000;
+
+struct Fp8Args {
+    const float* sa;        // [kb][R]
+    const float* sb;        // [G][nb][kb]
+    const int32_t* counts;  // nullptr: one group of R rows
+    int R, G, n, k;
+    int out_f32;
+    void* y;
+    int* status;
+    unsigned long long wait_limit_ns;
+};
+struct Fp8Maps {
+    CUtensorMap a, b;
+};
+
+template <int BN>
+struct Shape8 {
+    static constexpr int kStageBytes = kABytes8 + BN * kK8;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kTmemCols = 2 * BN;
+};
+
+template <int STAGES>
+struct Tail8 {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int row_off[kMaxE + 1];   // first row of each group
+    int tile_off[kMaxE + 1];  // first row tile of each group
+};
+
+template <int BN>
+constexpr size_t smem_bytes8() {
+    return 1024 + (size_t)Shape8<BN>::kStages * Shape8<BN>::kStageBytes +
+           sizeof(Tail8<Shape8<BN>::kStages>);
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+// the four 32-deep products of one block; the first starts the accumulator anew
+__device__ __forceinline__ void mma_block8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %3, %3;\n\t"
+        "setp.eq.b32 q, %3, %3;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %4, %5, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %6, %7, %3, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %8, %9, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "l"(a + 2), "l"(b + 2), "l"(a + 4), "l"(b + 4), "l"(a + 6),
+        "l"(b + 6)
+        : "memory");
+}
+__device__ __forceinline__ void commit8(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+// Instruction descriptor for kind::f8f6f4: fp32 accumulator (D format 1 in
+// [4,6)), A and B e4m3 (0 in [7,10) and [10,13)), both K-major, N >> 3 in
+// [17,23), M >> 4 in [24,29).
+constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// One tile of the launch.
+struct Tile8 {
+    int g, row0, rows, nt;
+};
+template <class TAIL>
+__device__ __forceinline__ Tile8 decode8(const TAIL* t, int G, int n_tiles, int tile) {
+    // row tiles of a group are neighbours: a weight tile is read from memory once
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {  // the last group that starts at or before this tile
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)t->tile_off[mid] * n_tiles <= tile)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int m_tiles = t->tile_off[lo + 1] - t->tile_off[lo];
+    const int local = tile - t->tile_off[lo] * n_tiles;
+    const int mt = local % m_tiles;
+    Tile8 r;
+    r.g = lo;
+    r.nt = local / m_tiles;
+    r.row0 = t->row_off[lo] + mt * kM8;
+    r.rows = min(kM8, t->row_off[lo + 1] - r.row0);
+    return r;
+}
+
+// 32 columns of a row from sums in registers
+template <int W>
+__device__ __forceinline__ void store_cols(const Fp8Args& a, size_t row, int col,
+                                           const uint64_t (&acc)[W]) {
+    const size_t base = row * (size_t)a.n + col;
+    if (a.out_f32) {
+        float* y = static_cast<float*>(a.y) + base;
+        if (a.n % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < W; i += 2) {
+                const float2 u = unpair(acc[i]), v = unpair(acc[i + 1]);
+                if (col + 2 * i < a.n)
+                    *reinterpret_cast<float4*>(y + 2 * i) = make_float4(u.x, u.y, v.x, v.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float2 u = unpair(acc[i]);
+                if (col + 2 * i < a.n) y[2 * i] = u.x;
+                if (col + 2 * i + 1 < a.n) y[2 * i + 1] = u.y;
+            }
+        }
+        return;
+    }
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + base;
+    if (a.n % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 u = unpair(acc[i + q]);
+                w[q] = pack_bf16x2(u.x, u.y);
+            }
+            if (col + 2 * i < a.n)
+                *reinterpret_cast<uint4*>(y + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float2 u = unpair(acc[i]);
+            if (col + 2 * i < a.n) y[2 * i] = __float2bfloat16_rn(u.x);
+            if (col + 2 * i + 1 < a.n) y[2 * i + 1] = __float2bfloat16_rn(u.y);
+        }
+    }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
+    const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Args a) {
+    using SH = Shape8<BN>;
+    constexpr int kStages = SH::kStages;
+    extern __shared__ uint8_t raw8[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw8) + 1023) &
+                                               ~(uintptr_t)1023);
+    auto* tail = reinterpret_cast<Tail8<kStages>*>(smem + (size_t)kStages * SH::kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &tail->abort;
+    int* status = a.status;
+    const uint64_t limit = a.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&tail->full[i], 1);
+            mbar_init(&tail->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tail->tfull[i], 1);
+            mbar_init(&tail->tempty[i], kEpiWarps8);
+        }
+        mbar_init(&tail->drain, 1);
+        tail->abort = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    if (warp == 0) {
+        // rows and row tiles of each group (exclusive prefix sums), cut at R rows
+        int rows = 0, tiles = 0;
+        for (int g0 = 0; g0 < a.G; g0 += 32) {
+            const int g = g0 + lane;
+            int c = g < a.G ? (a.counts != nullptr ? max(a.counts[g], 0) : a.R) : 0;
+            c = min(c, a.R);  // sums stay below 32 R + R; clamped to 64 bits below
+            long long ir = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, ir, o);
+                if (lane >= o) ir += v;
+            }
+            const long long all = __shfl_sync(0xffffffffu, ir, 31);
+            const int first = (int)min((long long)rows + ir - c, (long long)a.R);
+            const int last = (int)min((long long)rows + ir, (long long)a.R);
+            const int tl = (last - first + kM8 - 1) / kM8;
+            int it = tl;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, it, o);
+                if (lane >= o) it += v;
+            }
+            if (g < a.G) {
+                tail->row_off[g] = first;
+                tail->tile_off[g] = tiles + it - tl;
+            }
+            if (blockIdx.x == 0 && lane == 0 && (long long)rows + all > a.R)
+                set_status(status, MOE_ERR_DEVICE, SITE_GEMM_BOUNDS, a.R);
+            rows = (int)min((long long)rows + all, (long long)a.R);
+            tiles += __shfl_sync(0xffffffffu, it, 31);
+        }
+        if (lane == 0) {
+            tail->row_off[a.G] = rows;
+            tail->tile_off[a.G] = tiles;
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tail->tmem_base)),
+                     "n"(SH::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tail->tmem_base;
+    const int n_tiles = (a.n + BN - 1) / BN;
+    const int total = tail->tile_off[a.G] * n_tiles;
+    const int kb_n = (a.k + kK8 - 1) / kK8;
+
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == 0) {
+        // ------------------------------------------------ loads
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, issued = 0, issued_ph = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+                const Tile8 t = decode8(tail, a.G, n_tiles, tile);
+                for (int kb = 0; kb < kb_n; ++kb) {
+                    ok = mbar_wait_bounded(&tail->empty[s], ph ^ 1u, abort_flag, status,
+                                           SITE_GEMM_PRODUCER, limit);
+                    if (!ok) break;
+                    uint8_t* st = smem + (size_t)s * SH::kStageBytes;
+                    mbar_arrive_expect_tx(&tail->full[s], SH::kStageBytes);
+                    tma_load_2d(st, &maps.a, &tail->full[s], kb * kK8, t.row0);
+                    tma_load_3d(st + kABytes8, &maps.b, &tail->full[s], kb * kK8, t.nt * BN, t.g);
+                    issued |= 1u << s;
+                    issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok)  // no copy of this CTA may land after it has gone
+                for (int i = 0; i < kStages; ++i)
+                    if (issued & (1u << i))
+                        mbar_wait_bounded(&tail->full[i], (issued_ph >> i) & 1u, nullptr, status,
+                                          SITE_GEMM_DRAIN, kDrainNs8);
+        }
+      } else if (warp == 1) {
+        // ------------------------------------------------ products
+        if (lane == 0) {
+            int s = 0, blk = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint64_t ad0 = sw128_kmajor_desc(smem_u32(smem));
+            const uint64_t bd0 = sw128_kmajor_desc(smem_u32(smem) + kABytes8);
+            constexpr uint32_t idesc = idesc_e4m3_f32(kM8, BN);
+            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+                for (int kb = 0; kb < kb_n; ++kb, ++blk) {
+                    const int buf = blk & 1;
+                    ok = mbar_wait_bounded(&tail->tempty[buf], ((blk >> 1) & 1) ^ 1u, abort_flag,
+                                           status, SITE_GEMM_MMA, limit) &&
+                         mbar_wait_bounded(&tail->full[s], ph, abort_flag, status, SITE_GEMM_MMA,
+                                           limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)s * (SH::kStageBytes >> 4);
+                    mma_block8(tmem + (uint32_t)(buf * BN), ad0 + off, bd0 + off, idesc);
+                    commit8(&tail->empty[s]);
+                    commit8(&tail->tfull[buf]);
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+            commit8(&tail->drain);
+            mbar_wait_bounded(&tail->drain, 0u, nullptr, status, SITE_GEMM_DRAIN, limit);
+        }
+      }
+    } else {
+        // ------------------------------------------------ sums
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        constexpr int kCols = BN / 2;  // columns of this warp
+        const int wq = warp & 3, half = (warp - 4) >> 2;
+        const int nb = (a.n + 127) / 128;
+        int blk = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+            const Tile8 t = decode8(tail, a.G, n_tiles, tile);
+            const int r = wq * 32 + lane;
+            const int col0 = t.nt * BN + half * kCols;
+            const bool live = r < t.rows;
+            const float* sa = a.sa + t.row0 + r;
+            // columns behind n belong to no block of b: any scale will do
+            const float* sb = a.sb + ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * kb_n;
+            uint64_t acc[kCols / 2];
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
+            float sa_next = live ? __ldg(sa) : 0.f, sb_next = __ldg(sb);
+            for (int kb = 0; kb < kb_n; ++kb, ++blk) {
+                const float sc = sa_next * sb_next;
+                const uint64_t s2 = pair2(sc, sc);
+                if (kb + 1 < kb_n) {
+                    sa_next = live ? __ldg(sa + (size_t)(kb + 1) * a.R) : 0.f;
+                    sb_next = __ldg(sb + kb + 1);
+                }
+                const int buf = blk & 1;
+                ok = mbar_wait_bounded(&tail->tfull[buf], (blk >> 1) & 1, abort_flag, status,
+                                       SITE_GEMM_EPILOGUE, limit);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ta = tmem + (uint32_t)(buf * BN + half * kCols) +
+                                    ((uint32_t)(wq * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < kCols / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(ta + 32 * c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[16 * c + i] =
+                            fma_pair(pair2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                     s2, acc[16 * c + i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tail->tempty[buf]);
+            }
+            if (ok && live) store_cols(a, (size_t)t.row0 + r, col0, acc);
+        }
+    }
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "n"(SH::kTmemCols)
+                     : "memory");
+}
+
+template <int BN>
+cudaError_t launch_fp8(const void* a8, const void* b8, const Fp8Args& a, cudaStream_t s) {
+    Fp8Maps m;
+    if (!make_map_e4m3(&m.a, a8, (uint64_t)a.k, (uint64_t)a.R, 1, kM8, false) ||
+        !make_map_e4m3(&m.b, b8, (uint64_t)a.k, (uint64_t)a.n, (uint64_t)a.G, BN, true))
+        return cudaErrorInvalidValue;
+    auto kern = fp8_gemm_kernel<BN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem_bytes8<BN>());
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)num_sms()), dim3(kThreads8), smem_bytes8<BN>(), s, 1, m,
+                      a);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
+                           const float* b_scales, const int32_t* counts, int R, int G, int n,
+                           int k, int out_dt, void* y, void* status_ws, void* stream) {
+    if (R < 0 || G < 1 || G > kMaxE || n <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (out_dt != MOE_F32 && out_dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (counts == nullptr && G != 1) return MOE_ERR_INVALID_ARG;
+    // tiles are numbered in 32 bits; TMA coordinates are 32-bit
+    const long long m_tiles = ((long long)R + kM8 - 1) / kM8 + G;
+    if (k % 16 != 0 || m_tiles * (((long long)n + 63) / 64) > INT_MAX) return MOE_ERR_UNSUPPORTED;
+    if (R == 0) return MOE_OK;
+    const void* p16[] = {a, b, y};
+    for (const void* p : p16)
+        if (!is_device_ptr(p) || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+    const void* p4[] = {a_scales, b_scales};
+    for (const void* p : p4)
+        if (!is_device_ptr(p) || !aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+    if (counts != nullptr && (!is_device_ptr(counts) || !aligned(counts, 4)))
+        return MOE_ERR_INVALID_ARG;
+    if (status_ws != nullptr && (!is_device_ptr(status_ws) || !aligned(status_ws, 256)))
+        return MOE_ERR_INVALID_ARG;
+    Fp8Args f{};
+    f.sa = a_scales;
+    f.sb = b_scales;
+    f.counts = counts;
+    f.R = R;
+    f.G = G;
+    f.n = n;
+    f.k = k;
+    f.out_f32 = out_dt == MOE_F32 ? 1 : 0;
+    f.y = y;
+    f.status = static_cast<int*>(status_ws);
+    f.wait_limit_ns = kWaitLimitNs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // the widest tile that still gives every SM one
+    const long long rows_tiles = std::max((long long)std::min(G, R), ((long long)R + kM8 - 1) / kM8);
+    if (rows_tiles * ((n + 255) / 256) >= num_sms()) return ret(launch_fp8<256>(a, b, f, s));
+    if (rows_tiles * ((n + 127) / 128) >= num_sms()) return ret(launch_fp8<128>(a, b, f, s));
+    return ret(launch_fp8<64>(a, b, f, s));
+}
+
+}  // extern "C"

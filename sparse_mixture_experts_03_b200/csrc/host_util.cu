@@ -106,5 +106,22 @@ bool make_map_gate_up(CUtensorMap* m, const void* base, uint64_t G, uint64_t F, 
     return r == CUDA_SUCCESS;
 }
 
+// e4m3 matrices [G][rows][K] as {K, rows, G}: one box {128, box_rows, 1} brings
+// box_rows rows x 128 of K as one 128B-swizzled tile; K % 16 == 0, what lies
+// behind K, the rows or G reads as zeros.  three_d false: the first matrix alone, as {K, rows}.
+bool make_map_e4m3(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t G,
+                   uint32_t box_rows, bool three_d) {
+    auto fn = encode_fn();
+    if (fn == nullptr || rows == 0 || G == 0 || K % 16 != 0) return false;
+    cuuint64_t dims[3] = {K, rows, G};
+    cuuint64_t strides[2] = {K, K * rows};
+    cuuint32_t box[3] = {128, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, three_d ? 3 : 2, const_cast<void*>(base),
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
 
 }  // namespace moe

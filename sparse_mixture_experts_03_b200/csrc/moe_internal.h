@@ -260,6 +260,10 @@ bool make_map_rows_atoms(CUtensorMap* m, const void* base, uint64_t rows, uint64
                          uint32_t box_rows = 128);
 bool make_token_maps(CUtensorMap (&m)[kTokenBoxes], const void* base, uint64_t rows, uint64_t K);
 bool make_map_gate_up(CUtensorMap* m, const void* base, uint64_t G, uint64_t F, uint64_t K);
+// 8-bit (e4m3) matrices [G][rows][K] as {K, rows, G} (three_d) or {K, rows}:
+// boxes of box_rows rows x 128 of K, 128-byte swizzle.
+bool make_map_e4m3(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t G,
+                   uint32_t box_rows, bool three_d);
 // Epilogue pairs (epi0 for problem 0, epi1 for problem 1): SWIGLU/SWIGLU,
 // STORE_F32/SCATTER, SCATTER/SCATTER, SWIGLU_SAVE/SWIGLU_SAVE (KIND_FWD);
 // DSWIGLU/DSWIGLU, STORE_F32/SCATTER, SCATTER/SCATTER (KIND_DGRAD);

@@ -39,7 +39,9 @@ SYMBOLS = ["moe_workspace_bytes", "moe_workspace_layout", "moe_route", "moe_forw
            "moe_forward_train", "moe_backward_workspace_bytes", "moe_backward",
            "moe_set_backward_stage_events", "moe_dispatch_workspace_bytes", "moe_dispatch",
            "moe_experts_workspace_bytes", "moe_experts_forward", "moe_shared_workspace_bytes",
-           "moe_shared_forward", "moe_combine"]
+           "moe_shared_forward", "moe_combine", "moe_quantize_rows", "moe_swiglu_quantize_rows",
+           "moe_quantize_weight", "moe_matmul_fp8", "moe_few_max_tokens",
+           "moe_few_workspace_bytes", "moe_forward_few"]
 GATES = {"sigmoid": 0, "softmax": 1}  # MOE_GATE_SIGMOID, MOE_GATE_SOFTMAX_TOPK
 N_STAGE_EVENTS = 6
 STAGES = ["route", "permute", "gate_up", "down", "combine"]
@@ -112,6 +114,20 @@ def lib() -> ctypes.CDLL:
         L.moe_shared_forward.restype = i
         L.moe_combine.argtypes = [vp, i, vp, vp, i, i, i, i, vp, vp, vp]
         L.moe_combine.restype = i
+        L.moe_quantize_rows.argtypes = [vp, i, i, i, vp, vp, vp]
+        L.moe_quantize_rows.restype = i
+        L.moe_swiglu_quantize_rows.argtypes = [vp, vp, i, i, i, vp, vp, vp]
+        L.moe_swiglu_quantize_rows.restype = i
+        L.moe_quantize_weight.argtypes = [vp, i, i, i, i, vp, vp, vp]
+        L.moe_quantize_weight.restype = i
+        L.moe_matmul_fp8.argtypes = [vp] * 5 + [i] * 5 + [vp] * 3
+        L.moe_matmul_fp8.restype = i
+        L.moe_few_max_tokens.argtypes = [i] * 5
+        L.moe_few_max_tokens.restype = i
+        L.moe_few_workspace_bytes.argtypes = [i] * 6
+        L.moe_few_workspace_bytes.restype = sz
+        L.moe_forward_few.argtypes = [vp] * 8 + [i] * 11 + [vp] * 5 + [sz, vp]
+        L.moe_forward_few.restype = i
         _lib = L
     return _lib
 
@@ -440,6 +456,205 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, shared: Optional[torch.T
         y = torch.empty(T, d, dtype=out_dtype, device=rows.device)
     _check(lib().moe_combine(_ptr(rows), n_rows, _ptr(slot_row), _ptr(shared), T, d, k, _dt(y),
                              _ptr(y), _ptr(status_ws), _stream(stream)), "moe_combine")
+    return y
+
+
+# ---- 8-bit rows, weights and products (e4m3 codes, one fp32 scale per block of 128)
+
+E4M3 = torch.float8_e4m3fn
+
+
+def _want(name: str, t: torch.Tensor, shape, dtype, like: torch.Tensor) -> None:
+    """The tensor that an entry point expects: the library sees only its
+    pointer, so its shape, type and device are checked here."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _on_current(name: str, t: torch.Tensor) -> None:
+    """The library works on the current CUDA device."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                  scales: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_quantize_rows: (codes e4m3 [R, d], scales fp32 [ceil(d/128), R]) of
+    x [R, d] (bfloat16 or float32), one scale per 128 columns of a row."""
+    dt = _dt(x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [R, d], got {tuple(x.shape)}")
+    _on_current("x", x)
+    R, d = x.shape
+    if q is None:
+        q = torch.empty(R, d, dtype=E4M3, device=x.device)
+    else:
+        _want("q", q, (R, d), E4M3, x)
+    if scales is None:
+        scales = torch.empty(_blocks(d), R, dtype=torch.float32, device=x.device)
+    else:
+        _want("scales", scales, (_blocks(d), R), torch.float32, x)
+    _check(lib().moe_quantize_rows(_ptr(x), R, d, dt, _ptr(q), _ptr(scales), _stream(stream)),
+           "moe_quantize_rows")
+    return q, scales
+
+
+def swiglu_quantize_rows(gate_up: torch.Tensor, w: Optional[torch.Tensor] = None,
+                         q: Optional[torch.Tensor] = None,
+                         scales: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_swiglu_quantize_rows: (codes e4m3 [R, I], scales fp32 [ceil(I/128),
+    R]) of silu(gate) * up, gate_up bfloat16 [R, 2I]; w: fp32 [R] factors of
+    the rows' scales (gate weights)."""
+    dt = _dt(gate_up)
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2:
+        raise ValueError(f"gate_up must be [R, 2*inter], got {tuple(gate_up.shape)}")
+    _on_current("gate_up", gate_up)
+    R, inter = gate_up.shape[0], gate_up.shape[1] // 2
+    if w is not None:
+        _want("w", w, (R,), torch.float32, gate_up)
+    if q is None:
+        q = torch.empty(R, inter, dtype=E4M3, device=gate_up.device)
+    else:
+        _want("q", q, (R, inter), E4M3, gate_up)
+    if scales is None:
+        scales = torch.empty(_blocks(inter), R, dtype=torch.float32, device=gate_up.device)
+    else:
+        _want("scales", scales, (_blocks(inter), R), torch.float32, gate_up)
+    _check(lib().moe_swiglu_quantize_rows(_ptr(gate_up), _ptr(w), R, inter, dt, _ptr(q),
+                                          _ptr(scales), _stream(stream)),
+           "moe_swiglu_quantize_rows")
+    return q, scales
+
+
+def quantize_weight(W: torch.Tensor, q: Optional[torch.Tensor] = None,
+                    scales: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_quantize_weight: (codes e4m3, scales fp32 [..., ceil(n/128),
+    ceil(k/128)]) of W [n, k] or [G, n, k] (bfloat16 or float32)."""
+    dt = _dt(W)
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W must be [n, k] or [G, n, k], got {tuple(W.shape)}")
+    _on_current("W", W)
+    n, k = W.shape[-2:]
+    G = W.shape[0] if W.dim() == 3 else 1
+    lead = tuple(W.shape[:-2])
+    if q is None:
+        q = torch.empty(W.shape, dtype=E4M3, device=W.device)
+    else:
+        _want("q", q, W.shape, E4M3, W)
+    shape = lead + (_blocks(n), _blocks(k))
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=W.device)
+    else:
+        _want("scales", scales, shape, torch.float32, W)
+    _check(lib().moe_quantize_weight(_ptr(W), G, n, k, dt, _ptr(q), _ptr(scales),
+                                     _stream(stream)), "moe_quantize_weight")
+    return q, scales
+
+
+def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+               counts: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+               y: Optional[torch.Tensor] = None, status_ws: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """moe_matmul_fp8: y [R, n] in out_dtype (bfloat16 or float32), rows of a
+    (quantize_rows) times b [n, k] or [G, n, k] (quantize_weight); counts int32
+    [G] on the device: consecutive rows of each group."""
+    if a.dim() != 2 or b.dim() not in (2, 3):
+        raise ValueError(f"a must be [R, k] and b [n, k] or [G, n, k], got {tuple(a.shape)} "
+                         f"and {tuple(b.shape)}")
+    _on_current("a", a)
+    R, k = a.shape
+    n = b.shape[-2]
+    G = b.shape[0] if b.dim() == 3 else 1
+    _want("a", a, (R, k), E4M3, a)
+    _want("a_scales", a_scales, (_blocks(k), R), torch.float32, a)
+    _want("b", b, tuple(b.shape[:-1]) + (k,), E4M3, a)
+    _want("b_scales", b_scales, tuple(b.shape[:-2]) + (_blocks(n), _blocks(k)), torch.float32, a)
+    if counts is not None:
+        _want("counts", counts, (G,), torch.int32, a)
+    if y is None:
+        y = torch.empty(R, n, dtype=out_dtype, device=a.device)
+    else:
+        _want("y", y, (R, n), y.dtype, a)
+    _check(lib().moe_matmul_fp8(_ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), _ptr(counts),
+                                R, G, n, k, _dt(y), _ptr(y), _ptr(status_ws), _stream(stream)),
+           "moe_matmul_fp8")
+    return y
+
+
+# ---- the layer for a few tokens
+
+def few_max_tokens(d, E, k, inter, n_shared) -> int:
+    """The most tokens forward_few takes for these sizes (0: none)."""
+    return int(lib().moe_few_max_tokens(d, E, k, inter, n_shared))
+
+
+def few_workspace_bytes(T, d, E, k, inter, n_shared) -> int:
+    n = lib().moe_few_workspace_bytes(T, d, E, k, inter, n_shared)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_few_workspace_bytes")
+    return int(n)
+
+
+def forward_few(x: torch.Tensor, W_router: torch.Tensor, W_gate_up: torch.Tensor,
+                W_down: torch.Tensor, W_shared: Optional[torch.Tensor], k: int, n_group: int,
+                topk_group: int, inter: int, n_shared: int, scales=None,
+                out_dtype: torch.dtype = torch.float32, y: Optional[torch.Tensor] = None,
+                topk_idx: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None, gate: str = "sigmoid",
+                expert_bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_forward_few: forward() for up to few_max_tokens() tokens.  scales:
+    None for bfloat16 expert weights, or (s_gate_up, s_down, s_shared or None)
+    for e4m3 weights in the same layouts (quantize_weight)."""
+    _on_current("x", x)
+    T, d = x.shape
+    E = W_router.shape[0]
+    wt = torch.bfloat16 if scales is None else E4M3
+    sh = 3 * n_shared * inter * d
+    _want("W_router", W_router, (E, d), x.dtype, x)
+    _want("W_gate_up", W_gate_up, (E, 2 * inter, d), wt, x)
+    _want("W_down", W_down, (E, d, inter), wt, x)
+    if W_shared is not None:
+        _want("W_shared", W_shared, (sh,), wt, x)
+    s_gu = s_dn = s_sh = None
+    if scales is not None:
+        s_gu, s_dn, s_sh = scales
+        _want("s_gate_up", s_gu, (E, 2 * inter // 128, d // 128), torch.float32, x)
+        _want("s_down", s_dn, (E, d // 128, inter // 128), torch.float32, x)
+        if s_sh is not None:
+            _want("s_shared", s_sh, (sh // (128 * 128),), torch.float32, x)
+    if y is None:
+        y = torch.empty(T, d, dtype=out_dtype, device=x.device)
+    else:
+        _want("y", y, (T, d), y.dtype, x)
+    if topk_idx is not None:
+        _want("topk_idx", topk_idx, (T, k), torch.int32, x)
+    if topk_w is not None:
+        _want("topk_w", topk_w, (T, k), torch.float32, x)
+    if expert_bias is not None:
+        _want("expert_bias", expert_bias, (E,), torch.float32, x)
+    if workspace is None:
+        workspace = torch.empty(few_workspace_bytes(T, d, E, k, inter, n_shared),
+                                dtype=torch.uint8, device=x.device)
+    _check(lib().moe_forward_few(_ptr(x), _ptr(W_router), _ptr(W_gate_up), _ptr(W_down),
+                                 _ptr(W_shared), _ptr(s_gu), _ptr(s_dn), _ptr(s_sh), T, d, E, k,
+                                 n_group, topk_group, inter, n_shared, _dt(x), _dt(y),
+                                 GATES[gate], _ptr(expert_bias), _ptr(y), _ptr(topk_idx),
+                                 _ptr(topk_w), _ptr(workspace), workspace.numel(),
+                                 _stream(stream)), "moe_forward_few")
     return y
 
 
