@@ -9,37 +9,51 @@
 //   few_logits_kernel  the router logits (one CTA per expert, fp32 sums in a
 //                      fixed order) and the reset of the counters below
 //   few_layer_kernel   everything else, one persistent CTA per SM:
-//     - its producer warp streams weights into a ring of shared-memory stages
-//       (one bulk copy per weight row piece of up to 2 KB) and takes its work
-//       from one ticket counter: first units of 8 gate + 8 up rows, shared
-//       experts before routed ones, then units of down rows.  The shared
-//       experts need no routing, so their weights stream while the logits are
-//       still being made, and nothing that the second half waits for holds
-//       back its weights: the ring is full again when h is ready.
-//     - its 8 consumer warps split the reduction of each unit (every 8th block
+//     - its producer warp streams weights into a ring of shared-memory stages of
+//       up to 32 KB, unit after unit of 16 rows: 8 gate + 8 up rows of the shared
+//       experts, then of the routed ones, then down rows.  A stage is one TMA
+//       box (the rows as 128-byte swizzled atoms): row by row with
+//       cp.async.bulk each copy took about 65 ns whatever its size, 4 TB/s
+//       in all.  The shared experts need no routing, so their weights
+//       stream while the logits are still being made, and nothing that the
+//       down rows wait for holds back their weights: the ring is full again
+//       when h is ready.
+//     - its 8 product warps split the reduction of each unit (every 8th block
 //       of 128) and multiply on mma.sync m16n8k16: the weights are the 16 rows
 //       of A, read from the stage as 16 bytes per lane, the tokens the 8
 //       columns of B.  The tensor work is a few percent of what the SM can do;
 //       tcgen05 tiles of 128 rows would only make the units coarser.
-//     - every consumer warp in turn adds the 8 partial sums of a unit in warp
+//     - 4 sum warps take the units in turn and add their 8 partial sums in warp
 //       order; gate and up rows of a feature meet in one lane, h = silu(g) u is
 //       rounded once to bf16 (the operand type of the down product).  Down
-//       sums go, times the gate weight, into fp32 slots [token][S + k][d]; the
-//       last unit of a 16-column piece of y adds the slots, shared experts
-//       first, then the token's choices in top-k order, and rounds once.
+//       sums go, times the gate weight, into fp32 slots [token][S + k][d]; y adds
+//       a token's slots, shared experts first, then its choices in top-k
+//       order, and rounds once.
+//       What other CTAs wait for (h, the slots) is told once per run of units:
+//       a fence behind the stores and a counter take a microsecond or two, more
+//       than streaming a unit.  (Told per unit, by the product warps, it made
+//       T = 1 take 83 us and T = 16 432 us; per unit but by the sum warps 65
+//       and 322.)
+//   The units of each part (shared up, routed up, down, y) are cut into gridDim.x
+//   runs of neighbours; a CTA takes a run by a ticket, one atomic per part.
 //
 // Results do not depend on which CTA took which ticket: every unit is summed
 // the same way wherever it runs, and the slots are added in order.
 //
 // Waits between CTAs (down units wait for the h of their expert) cannot
-// deadlock whatever else runs on the GPU: tickets are handed out in order, so
-// all that a ticket waits for is in the hands of CTAs that already run and
-// that never wait for a later ticket.  All waits are bounded.
+// deadlock whatever else runs on the GPU: a CTA goes to the next part when all
+// runs of this one are taken, so all that a run waits for is in the hands of
+// CTAs that already run, and they do it before they wait for anything later.
+// All waits are bounded.
 //
 // 8-bit weights (e4m3, one fp32 scale per 128 x 128 block) take half the
-// bytes: a stage row of 2 KB holds 2048 of them, the codes become bf16 (exact)
-// on the way to the same products, and each 128-block's sum is scaled in fp32
-// before it is added; the scales travel with the stage.
+// bytes: a stage row of 2 KB holds 2048 of them, and each 128-block's sum is
+// scaled in fp32 before it is added; the scales travel with the stage.  The
+// codes become fp16, one instruction for two of them (exact; bf16 takes four
+// or five, as much time as the stream), so the tokens are fp16 too: each row
+// times a power of two that brings its largest magnitude to [2^14, 2^15).
+// bf16's 8 bits fit fp16's 11 down to 2^-28 of the largest magnitude, and what
+// lies below is off by at most 2^-39 of it, far less than the fp32 sums are.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <limits.h>
@@ -48,36 +62,47 @@
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
-#include "route_select.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kFewMaxT = 16;
-constexpr int kWarps = 8;                       // consumer warps
-constexpr int kFewThreads = 32 * (kWarps + 1);  // + the producer warp
+constexpr int kWarps = 8;                       // product warps
+constexpr int kSumWarps = 4;
+constexpr int kSumBufs = 2;                     // partial sums in flight (a sum warp frees its
+                                                // buffer before it stores and tells)
+constexpr int kFewThreads = 32 * (kWarps + kSumWarps + 1);  // + the producer warp
 constexpr int kRowBytes = 2048;                 // bytes of one weight row in a stage
-// Row pitch: 64 bytes more than a multiple of 128, so that the 8 lanes of a
-// quarter warp (2 rows x 64 bytes) read 8 different 16-byte bank groups.
-constexpr int kRowPitch = kRowBytes + 64;
-constexpr int kStageBytes = 16 * kRowPitch;
+constexpr int kAtomBytes = 16 * 128;            // 16 rows x 128 bytes
+constexpr int kStageBytes = 16 * kRowBytes;     // [atom][16 rows][128 bytes]
 constexpr int kMaxStages = 6;
 constexpr int kMaxShared = 64;                  // shared experts
 constexpr int kMaxEntries = kMaxShared + kFewMaxT * kMaxK;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kLogitThreads = 256;
 
-// Control words (reset by few_logits_kernel): the ticket counter, finished
-// gate/up units per entry, finished entries per 16 columns of y.
-constexpr int kCtrlTicket = 0;
-constexpr int kCtrlH = 32;
-constexpr int kCtrlY = kCtrlH + kMaxEntries;
+// The parts of the work, and what a stage or a unit is.
+enum Part : int { PART_SHARED_UP, PART_ROUTED_UP, PART_DOWN, PART_Y, kParts };
+enum What : int {
+    WHAT_END = -1,
+    WHAT_DOWN = 0,  // 16 down rows of an entry
+    WHAT_UP = 1,    // 8 gate and the 8 matching up rows
+    WHAT_TOLD = 2,  // the end of a run: tell the other CTAs
+    WHAT_Y = 3,     // 16 columns of y
+};
+// Control words (reset by few_logits_kernel), each counter on a sector of its
+// own: the tickets of each part, the sum warps that finished a down run, finished
+// gate/up units per entry.
+constexpr int kCtrlTicket = 0;  // + 8 * part
+constexpr int kCtrlDown = 8 * kParts;
+constexpr int kCtrlH = kCtrlDown + 8;
+constexpr int kCtrlWords = kCtrlH + kMaxEntries;
 
 struct FewArgs {
+    // Boxes of 16 rows x the atoms of a piece: up [part] {128 bytes, rows, gate |
+    // up, atoms}, down [part] {128 bytes, rows, atoms}; 0 shared, 1 routed experts.
+    CUtensorMap up_map[2], down_map[2];
     const __nv_bfloat16* x;
-    const void* w_gate_up;  // [E, 2 I, d]
-    const void* w_down;     // [E, d, I]
-    const void* w_shared;   // [2 S I, d], then [d, S I]
     const float* s_gate_up; // 8-bit weights: scales [E, 2 I / 128, d / 128]
     const float* s_down;    // [E, d / 128, I / 128]
     const float* s_shared;  // [2 S I / 128, d / 128], then [d / 128, S I / 128]
@@ -85,7 +110,6 @@ struct FewArgs {
     const float* bias;
     int T, d, E, k, G, TG, gate, I, S, out_f32;
     int stages;
-    int tile_rows;          // 16-row pieces of a down ticket
     void* y;
     int32_t* idx_out;
     float* w_out;
@@ -129,16 +153,112 @@ __global__ void __launch_bounds__(kLogitThreads) few_logits_kernel(
     }
 }
 
+// ---------------------------------------------------------------- routing
+// fp32 as an unsigned number of the same order (NaN and -0 as -inf and +0)
+__device__ __forceinline__ uint32_t ordered(float v) {
+    if (v != v) v = -INFINITY;
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+// The k experts of one token and their weights, by one warp: the rules of the
+// router kernels (largest keys inside the topk_group groups of largest maximum,
+// ties to the lower index), as short loops: this code runs once per launch and
+// its instructions come from L2, so its length is its time.  key [E] is scratch
+// and starts as the logits.
+__device__ __noinline__ void choose(uint32_t* key, int lane, int E, int k, int G, int TG, int gate,
+                                    const float* bias, int* idx, float* w) {
+    const int gsz = E / G;
+    float* logit = reinterpret_cast<float*>(key);
+    // the token's logits stay in registers of the lanes for the weights
+    float mine[kMaxE / 32];
+#pragma unroll
+    for (int j = 0; j < kMaxE / 32; ++j) {
+        const int e = lane + 32 * j;
+        mine[j] = 0.f;
+        if (e < E) {
+            const float l = logit[e];
+            mine[j] = l;
+            // the gate score is monotone in the logit: without a bias the logit is the key
+            const float g = bias == nullptr ? l
+                            : (gate == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-l)) : l) + bias[e];
+            key[e] = ordered(g);
+        }
+    }
+    __syncwarp();
+    uint32_t best = 0;  // ordered() never gives 0: it marks what is out
+    if (lane < G)
+        for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) best = max(best, key[e]);
+    uint32_t kept = 0;
+#pragma unroll 1
+    for (int r = 0; r < TG; ++r) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int g = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+        kept |= 1u << g;
+        if (lane == g) best = 0;
+    }
+    for (int e = lane; e < E; e += 32)
+        if (!((kept >> (e / gsz)) & 1u)) key[e] = 0;
+    float l = 0.f;  // lane r: the r-th choice's logit
+#pragma unroll 1
+    for (int r = 0; r < k; ++r) {
+        __syncwarp();
+        uint32_t b = 0;
+        int be = kMaxE;
+        for (int e = lane; e < E; e += 32)
+            if (key[e] > b) {
+                b = key[e];
+                be = e;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, b);
+        const int e = (int)__reduce_min_sync(0xffffffffu, b == top ? (uint32_t)be : (uint32_t)kMaxE);
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < kMaxE / 32; ++j)
+            if (j == e >> 5) v = mine[j];
+        v = __shfl_sync(0xffffffffu, v, e & 31);
+        if (lane == r) {
+            l = v;
+            idx[r] = e;
+        }
+        if (lane == (e & 31)) key[e] = 0;
+    }
+    // weights in the router kernels' order of operations
+    float s = 0.f;
+    if (gate == MOE_GATE_SIGMOID) {
+        s = 1.f / (1.f + expf(-l));
+    } else {
+        float m = __shfl_sync(0xffffffffu, l, 0);
+        for (int r = 1; r < k; ++r) m = fmaxf(m, __shfl_sync(0xffffffffu, l, r));
+        s = expf(l - m);
+    }
+    float sum = 0.f;
+    for (int r = 0; r < k; ++r) sum += __shfl_sync(0xffffffffu, s, r);
+    if (lane < k) w[lane] = s / sum;
+}
+
 // ---------------------------------------------------------------- copies
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
+__device__ __forceinline__ void box_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int row,
+                                       int atom) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-        ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(atom)
         : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void box_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int row,
+                                       int atom) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %3, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(atom)
+        : "memory");
+}
+__device__ __forceinline__ void box_4d_to_l2(const CUtensorMap* map, int row, int atom) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %1, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(0), "r"(row), "r"(atom)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_scale(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
@@ -149,8 +269,11 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void consumers_sync() {
+__device__ __forceinline__ void products_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+__device__ __forceinline__ void sums_sync() {
+    asm volatile("bar.sync 2, %0;" ::"n"(32 * kSumWarps) : "memory");
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -161,38 +284,43 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-// four e4m3 codes as two bf16 pairs (exact: 4 significant bits; NaN stays NaN)
+// four e4m3 codes as two fp16 pairs (exact; NaN stays NaN)
 __device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu),
-                                                      __NV_E4M3);
-    const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> 16),
-                                                      __NV_E4M3);
-    const float2 f0 = __half22float2(__half2(h0)), f1 = __half22float2(__half2(h1));
-    lo = pack_bf16x2(f0.x, f0.y);
-    hi = pack_bf16x2(f1.x, f1.y);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
 
 // ---------------------------------------------------------------- work
-// A unit is 16 weight rows over their whole reduction.  up: gate/up rows
-// (8 gate + the 8 matching up rows) of feature 8 * tile; else down rows
-// [16 * tile, 16 * tile + 16).
-struct Unit {
-    int up;     // 1 gate/up, 0 down, -1 no more work
-    int entry;  // 0 .. S-1 shared experts, then the routed experts that have tokens
-    int tile;
-};
-
+// A unit is 16 weight rows over their whole reduction: gate/up rows (8 gate + the
+// 8 matching up rows) of features 8 * tile .., or down rows 16 * tile ...  It
+// belongs to an entry: 0 .. S-1 the shared experts, then the routed experts that
+// have tokens, in order.  Stages and units carry (what, entry, tile, piece).
 struct Smem {
     uint8_t* ring;
     uint4* b;        // operand B: x (gate/up units), then the h of one entry
-    float4* red;     // [2][kWarps][NT][32]
+    float4* red;     // [kSumBufs][kWarps][NT][32]
     float* scales;   // [stages][32]
     int4* info;      // [stages]
     uint64_t* full;
     uint64_t* empty;
     uint64_t* routed;  // the entry list is there
-    uint64_t* meet;    // the consumer warps, once or twice per unit
+    uint32_t* keys;    // [T][E] logits, then selection keys
+    uint64_t* meet;    // the product warps, around a new operand B
+    uint64_t* sum_full;   // [kSumWarps]: a unit's partial sums are there
+    uint64_t* sum_empty;  // [kSumBufs]
+    int4* unit;        // [kSumWarps]: the unit
+    float* unscale;    // [kFewMaxT] 8-bit weights: 1 / the power of two of operand B's row
     int* s_idx;      // [T][k]
     float* s_w;
     uint32_t* s_mask;  // [E] tokens of each expert
@@ -203,10 +331,11 @@ struct Smem {
 
 template <int NT>
 __host__ __device__ constexpr int red_bytes() {
-    return 2 * kWarps * NT * 32 * 16;  // also holds the logits: T * E * 4 <= 8 NT * 256 * 4
+    return kSumBufs * kWarps * NT * 32 * 16;
 }
-constexpr int kSmallBytes = kMaxStages * (32 * 4 + 16 + 16) + 64 + kFewMaxT * kMaxK * 8 +
-                            kMaxE * 4 + kMaxEntries * 4 + 64;
+constexpr int kSmallBytes = 1024 + kMaxStages * (32 * 4 + 16 + 16) + 64 + kSumWarps * 24 + kSumBufs * 8 +
+                            kFewMaxT * 4 + kFewMaxT * kMaxK * 8 + kMaxE * 4 + kMaxEntries * 4 +
+                            64;
 
 template <int NT>
 __host__ __device__ inline int b_bytes(int d, int I) {
@@ -231,6 +360,14 @@ __device__ __forceinline__ Smem carve(uint8_t* p, int stages, int d, int I) {
     s.routed = reinterpret_cast<uint64_t*>(p);
     s.meet = s.routed + 1;
     p += 16;
+    s.unit = reinterpret_cast<int4*>(p);
+    p += kSumWarps * 16;
+    s.sum_full = reinterpret_cast<uint64_t*>(p);
+    p += kSumWarps * 8;
+    s.sum_empty = reinterpret_cast<uint64_t*>(p);
+    p += kSumBufs * 8;
+    s.unscale = reinterpret_cast<float*>(p);
+    p += kFewMaxT * 4;
     s.scales = reinterpret_cast<float*>(p);
     p += kMaxStages * 32 * 4;
     s.s_idx = reinterpret_cast<int*>(p);
@@ -243,15 +380,20 @@ __device__ __forceinline__ Smem carve(uint8_t* p, int stages, int d, int I) {
     p += kMaxEntries * 4;
     s.n_entries = reinterpret_cast<int*>(p);
     s.abort = s.n_entries + 1;
+    p += 16;
+    s.keys = reinterpret_cast<uint32_t*>(p);
     return s;
 }
 
+constexpr int kAhead = 4;  // units that are on their way to L2 ahead of the ring
+
 // Pieces of a reduction of K elements: n of len elements (a multiple of 128)
-// whose rows fit a stage; the last may be shorter.
+// whose rows fit a stage; the last may be shorter (its box reads on into what
+// follows, or zeros, and that is not used).
 struct Pieces {
     int n, len;
 };
-__device__ __forceinline__ Pieces pieces(int K, int esz) {
+__host__ __device__ __forceinline__ Pieces pieces(int K, int esz) {
     Pieces p;
     p.n = (K * esz + kRowBytes - 1) / kRowBytes;
     p.len = ((K + p.n - 1) / p.n + 127) / 128 * 128;
@@ -282,71 +424,98 @@ template <bool FP8>
 __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int lane) {
     constexpr int esz = FP8 ? 1 : 2;
     const int d = a.d, I = a.I, S = a.S;
-    const int up_tiles = I / 8, down_tickets = d / 16 / a.tile_rows;
+    const int up_tiles = I / 8, down_tiles = d / 16;
     const int shared_units = S * up_tiles;
     const Pieces pu = pieces(d, esz), pd = pieces(I, esz);
-    const char* wgu = static_cast<const char*>(a.w_gate_up);
-    const char* wdn = static_cast<const char*>(a.w_down);
-    const char* wsh = static_cast<const char*>(a.w_shared);
     const size_t SI = (size_t)S * I;
-    // The first tickets are shared gate/up units: this CTA's part of them goes
-    // to L2 now, while the logits are being made.  (Which CTA takes a ticket is
-    // open, but together they take these.)
-    if (lane < 16) {
-        for (int u = blockIdx.x; u < shared_units && u < 2 * (int)gridDim.x; u += gridDim.x) {
-            const size_t row = (size_t)u * 8 + (lane & 7) + (lane >= 8 ? SI : 0);
-            prefetch_l2(wsh + row * d * esz, (uint32_t)(d * esz));
-        }
+    const int atoms_u = pu.len * esz / 128, atoms_d = pd.len * esz / 128;
+    auto run_start = [&](int run, int units) {
+        return (int)((long long)run * units / gridDim.x);
+    };
+    // The first run is one of shared gate/up units: its first rows go to L2 now,
+    // while the logits are being made.  (Which CTA takes a run is open, but
+    // together they take these.)
+    if (lane == 0) {
+        const int last = run_start(blockIdx.x + 1, shared_units);
+        int u = run_start(blockIdx.x, shared_units);
+        for (int i = 0; i < kAhead && u < last; ++i, ++u)
+            for (int c = 0; c < pu.n; ++c) box_4d_to_l2(&a.up_map[0], u * 8, c * atoms_u);
     }
     pdl_wait();  // the control words are reset
     int slot = 0, phase = 0;
-    int n_entries = -1;  // unknown until the routing is there
-    int ticket = 0, next = 0;
+    int part = 0, ticket = 0, ahead = 0;
+    int total = shared_units;
+    bool ok = true, took_ahead = false;
     if (lane == 0) ticket = atomicAdd(a.ctrl + kCtrlTicket, 1);
-    for (;;) {
-        ticket = __shfl_sync(0xffffffffu, ticket, 0);
-        if (ticket >= shared_units && n_entries < 0) {
-            bool ok = mbar_wait_bounded(s.routed, 0, s.abort, a.status, SITE_GEMM_PRODUCER,
-                                        a.wait_limit_ns);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            n_entries = *s.n_entries;
+    // a stage that carries no weights
+    auto put_word = [&](int what, int tile) {
+        ok = mbar_wait_bounded(s.empty + slot, phase ^ 1, s.abort, a.status, SITE_GEMM_PRODUCER,
+                               a.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
+            s.info[slot] = make_int4(what, part, tile, 0);
+            mbar_arrive(s.full + slot);
         }
-        const bool is_up = ticket < shared_units || ticket < n_entries * up_tiles;
-        const int rest = ticket - (is_up ? 0 : n_entries * up_tiles);
-        if (!is_up && rest >= n_entries * down_tickets) break;
-        if (lane == 0) next = atomicAdd(a.ctrl + kCtrlTicket, 1);  // used one ticket later
-        const int entry = rest / (is_up ? up_tiles : down_tickets);
-        const int within = rest - entry * (is_up ? up_tiles : down_tickets);
-        const int expert = entry < S ? -1 : s.list[entry];
+        if (FP8) copies_arrive(s.full + slot);
+        if (++slot == a.stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    while (ok && part < kParts) {
+        ticket = __shfl_sync(0xffffffffu, ticket, 0);
+        if (ticket >= (int)gridDim.x) {  // all runs of this part are taken
+            ticket = ahead;
+            if (!took_ahead && lane == 0 && part + 1 < kParts)
+                ticket = atomicAdd(a.ctrl + kCtrlTicket + 8 * (part + 1), 1);
+            took_ahead = false;
+            ++part;
+            if (part == PART_ROUTED_UP) {
+                ok = mbar_wait_bounded(s.routed, 0, s.abort, a.status, SITE_GEMM_PRODUCER,
+                                       a.wait_limit_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+            total = part == PART_ROUTED_UP ? (*s.n_entries - S) * up_tiles
+                    : part == PART_DOWN    ? *s.n_entries * down_tiles
+                                           : down_tiles;
+            continue;
+        }
+        const int first = run_start(ticket, total), last = run_start(ticket + 1, total);
+        // the next part's ticket: the answer is there when this run is done (not
+        // so this part's: the CTAs that start first would take two runs each)
+        if (!took_ahead && part + 1 < kParts) {
+            if (lane == 0) ahead = atomicAdd(a.ctrl + kCtrlTicket + 8 * (part + 1), 1);
+            took_ahead = true;
+        }
+        const bool is_up = part < PART_DOWN;
         const Pieces p = is_up ? pu : pd;
         const int K = is_up ? d : I;
-        const int n_tiles = is_up ? 1 : a.tile_rows;
-        bool ok = true;
-        for (int i = 0; i < n_tiles && ok; ++i) {
-            const int tile = is_up ? within : within * a.tile_rows + i;
-            // this lane's weight row and (8-bit) its row of scales
-            const char* row;
-            const float* sc = nullptr;
-            const int r = lane & 15;
-            if (is_up) {
-                const size_t f = (size_t)tile * 8 + (r & 7);
-                const size_t F = expert < 0 ? SI : (size_t)I;
-                const size_t in = f + (expert < 0 ? (size_t)entry * I : 0);
-                const size_t g = (expert < 0 ? 0 : (size_t)expert * 2 * I) + in + (r >= 8 ? F : 0);
-                row = (expert < 0 ? wsh : wgu) + g * d * esz;
-                if (FP8) {
+        const int tiles = is_up ? up_tiles : down_tiles;
+        for (int u = first; u < last && ok; ++u) {
+            if (part == PART_Y) {
+                put_word(WHAT_Y, u);
+                continue;
+            }
+            const int entry = u / tiles + (part == PART_ROUTED_UP ? S : 0);
+            const int tile = u % tiles;
+            const int expert = entry < S ? -1 : s.list[entry];
+            // the unit's first weight row (of the gate rows, or the down rows)
+            const int row = is_up ? (expert < 0 ? entry * I : expert * 2 * I) + tile * 8
+                                  : (expert < 0 ? 0 : expert * d) + tile * 16;
+            const CUtensorMap* map = (is_up ? a.up_map : a.down_map) + (expert < 0 ? 0 : 1);
+            const int atom0 = !is_up && expert < 0 ? entry * (I * esz / 128) : 0;
+            const int atoms = is_up ? atoms_u : atoms_d;
+            const float* sc = nullptr;  // 8-bit: this lane's row of scales
+            if (FP8) {
+                if (is_up) {
                     // lanes 0..15: the gate rows' scales, 16..31: the up rows'
-                    const size_t first = (expert < 0 ? 0 : (size_t)expert * 2 * I) +
-                                         (size_t)tile * 8 +
-                                         (expert < 0 ? (size_t)entry * I : 0) +
-                                         (lane >= 16 ? F : 0);
-                    sc = (expert < 0 ? a.s_shared : a.s_gate_up) + first / 128 * (d / 128);
-                }
-            } else {
-                const size_t o = (size_t)tile * 16 + r;
-                row = expert < 0 ? wsh + (2 * SI * d + o * SI + (size_t)entry * I) * esz
-                                 : wdn + ((size_t)expert * d + o) * I * esz;
-                if (FP8) {
+                    const size_t F = expert < 0 ? SI : (size_t)I;
+                    const size_t row0 = (expert < 0 ? (size_t)entry * I : (size_t)expert * 2 * I) +
+                                        (size_t)tile * 8 + (lane >= 16 ? F : 0);
+                    sc = (expert < 0 ? a.s_shared : a.s_gate_up) + row0 / 128 * (d / 128);
+                } else {
                     const size_t ob = (size_t)tile * 16 / 128;
                     sc = expert < 0 ? a.s_shared + 2 * SI / 128 * (d / 128) + ob * (SI / 128) +
                                           (size_t)entry * I / 128
@@ -360,13 +529,15 @@ __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int la
                 if (!ok) break;
                 const int k0 = c * p.len, len = min(p.len, K - k0);
                 if (lane == 0) {
-                    s.info[slot] = make_int4(is_up ? 1 : 0, entry, tile, c);
-                    mbar_arrive_expect_tx(s.full + slot, (uint32_t)(16 * len * esz));
+                    s.info[slot] = make_int4(is_up ? WHAT_UP : WHAT_DOWN, entry, tile, c);
+                    mbar_arrive_expect_tx(s.full + slot, (uint32_t)(atoms * kAtomBytes));
+                    uint8_t* dst = s.ring + slot * kStageBytes;
+                    if (is_up)
+                        box_4d(dst, map, s.full + slot, row, atom0 + c * atoms);
+                    else
+                        box_3d(dst, map, s.full + slot, row, atom0 + c * atoms);
                 }
                 __syncwarp();
-                if (lane < 16)
-                    bulk_copy(s.ring + slot * kStageBytes + lane * kRowPitch,
-                              row + (size_t)k0 * esz, (uint32_t)(len * esz), s.full + slot);
                 if (FP8) {
                     if ((lane & 15) < len / 128 && (is_up || lane < 16))
                         copy_scale(s.scales + slot * 32 + lane, sc + k0 / 128 + (lane & 15));
@@ -379,18 +550,11 @@ __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int la
             }
         }
         if (!ok) break;
-        ticket = next;
+        if (part != PART_Y) put_word(WHAT_TOLD, 0);
+        if (lane == 0) ticket = atomicAdd(a.ctrl + kCtrlTicket + 8 * part, 1);
     }
-    // the end of the work, or of a CTA that gave up: a stage without data
-    bool ok = mbar_wait_bounded(s.empty + slot, phase ^ 1, s.abort, a.status, SITE_GEMM_PRODUCER,
-                                a.wait_limit_ns);
-    if (__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) {
-            s.info[slot] = make_int4(-1, 0, 0, 0);
-            mbar_arrive(s.full + slot);
-        }
-        if (FP8) copies_arrive(s.full + slot);
-    } else {
+    if (ok) put_word(WHAT_END, 0);
+    if (!ok) {
         // gave up: wait for this CTA's own copies before its memory goes away
         // (the stages before `slot`, newest first; those never filled time out)
         int q = slot, ph = phase;
@@ -404,28 +568,86 @@ __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int la
     }
 }
 
-// ---------------------------------------------------------------- consumers
+// ---------------------------------------------------------------- products
 // Rows [T][K] of bf16 into operand B: the 8 tokens of a column group as the
-// lanes (token, quarter) hold them.  A group of reduction elements (64 bytes
-// of a weight row: 32 bf16, 64 e4m3) is split into quarters of consecutive
-// elements, the same for A and B, which permutes the reduction inside the
-// group and nothing else.  Piece j (8 elements, 16 bytes) of a quarter of group
-// i of token t is b[((i * PPQ + j) * NT + t / 8) * 32 + (t % 8) * 4 + quarter],
-// PPQ = pieces per quarter (1 or 2).
+// lanes (token, quarter) hold them.  An atom (128 bytes of a weight row: 64
+// bf16, 128 e4m3) is 8 chunks of 16 bytes; lane quarter c takes chunks 2c and
+// 2c + 1 as its part of two groups of products, the same for A and B, which
+// permutes the reduction inside the atom and nothing else.  (With chunks c and
+// c + 4 the two rows that a quarter warp reads would swizzle to the same banks.)
+// Piece j (8 elements, 16 bytes of operand B) of the chunk of group g (atom
+// g / 2) of token t is b[((g * PPQ + j) * NT + t / 8) * 32 + (t % 8) * 4 + c],
+// PPQ = pieces per chunk (1 or 2).  A warp per token; 8-bit weights: as fp16
+// times a power of two (1 / it goes to unscale).
 template <int NT, bool FP8>
-__device__ __forceinline__ void fill_b(uint4* b, const __nv_bfloat16* src, size_t ld, int K,
-                                       uint32_t mask, int n_tok, bool zero_rest, int tid) {
+__device__ __forceinline__ void fill_b(const Smem& s, const __nv_bfloat16* src, size_t ld, int K,
+                                       uint32_t mask, int n_tok, bool zero_rest, int warp,
+                                       int lane) {
     constexpr int PPQ = FP8 ? 2 : 1;
-    const int per_tok = K / 8;
-    for (int i = tid; i < n_tok * per_tok; i += 32 * kWarps) {
-        const int t = i / per_tok, p = i - t * per_tok;
+    for (int t = warp; t < n_tok; t += kWarps) {
         const bool have = (mask >> t) & 1u;
         if (!have && !zero_rest) continue;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (have) v = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)t * ld) + p);
-        const int grp = p / (4 * PPQ), in = p - grp * 4 * PPQ;
-        const int quarter = in / PPQ, j = in - quarter * PPQ;
-        b[((grp * PPQ + j) * NT + (t >> 3)) * 32 + (t & 7) * 4 + quarter] = v;
+        const uint4* row = reinterpret_cast<const uint4*>(src + (size_t)t * ld);
+        const int n = K / 8;
+        // up to 2048 elements are read once, kPass pieces per lane
+        constexpr int kPass = 8;
+        uint4 v[kPass];
+        auto read = [&](int p0) {
+#pragma unroll
+            for (int i = 0; i < kPass; ++i) {
+                const int p = p0 + 32 * i + lane;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (have && p < n) v[i] = __ldcg(row + p);
+            }
+        };
+        read(0);
+        float scale = 1.f;
+        if (FP8 && have) {
+            uint32_t m = 0;
+            for (int p0 = 0;;) {
+#pragma unroll
+                for (int i = 0; i < kPass; ++i) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        m = max(m, max(w[q] & 0x7fffu, (w[q] >> 16) & 0x7fffu));
+                }
+                p0 += 32 * kPass;
+                if (p0 >= n) break;
+                read(p0);
+            }
+            if (n > 32 * kPass) read(0);
+            // exponent field of the largest magnitude (bf16); infinities and
+            // NaN, whose results are not numbers anyway, keep a scale of 1
+            const int e = (int)(__reduce_max_sync(0xffffffffu, m) >> 7);
+            const int up = e == 255 ? 0 : 14 - (max(e, 27) - 127);
+            scale = __uint_as_float((uint32_t)(127 + up) << 23);
+            if (lane == 0) s.unscale[t] = __uint_as_float((uint32_t)(127 - up) << 23);
+        }
+        for (int p0 = 0;;) {
+#pragma unroll
+            for (int i = 0; i < kPass; ++i) {
+                const int p = p0 + 32 * i + lane;
+                if (p >= n) continue;
+                uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                if (FP8) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const __half2 h =
+                            __floats2half2_rn(__uint_as_float(w[q] << 16) * scale,
+                                              __uint_as_float(w[q] & 0xffff0000u) * scale);
+                        w[q] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                }
+                const int chunk = p / PPQ, j = p % PPQ;
+                const int grp = (chunk >> 3) * 2 + (chunk & 1), c = (chunk >> 1) & 3;
+                s.b[((grp * PPQ + j) * NT + (t >> 3)) * 32 + (t & 7) * 4 + c] =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            p0 += 32 * kPass;
+            if (p0 >= n) break;
+            read(p0);
+        }
     }
 }
 
@@ -435,15 +657,19 @@ template <int NT, bool FP8>
 __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, const float* scales,
                                           int k0, int len, bool up, int warp, int lane,
                                           float (&acc)[NT][4]) {
-    const uint8_t* r0 = st + (lane >> 2) * kRowPitch + (lane & 3) * 16;
-    const uint8_t* r1 = r0 + 8 * kRowPitch;
+    const int row = lane >> 2;
+    const uint8_t* r0 = st + row * 128;
+    const uint8_t* r1 = r0 + 8 * 128;
+    // this lane's chunk of group 0 and 1 of an atom, swizzled
+    const int pos[2] = {((2 * (lane & 3)) ^ row) << 4, ((2 * (lane & 3) + 1) ^ row) << 4};
     const int first = k0 / 128;
     for (int j = (warp - first) & 7; j < len / 128; j += kWarps) {
         if constexpr (!FP8) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {  // 32 elements each
-                const uint4 lo = *reinterpret_cast<const uint4*>(r0 + j * 256 + g * 64);
-                const uint4 hi = *reinterpret_cast<const uint4*>(r1 + j * 256 + g * 64);
+            for (int g = 0; g < 4; ++g) {  // 32 elements each, 2 atoms
+                const int at = (2 * j + (g >> 1)) * kAtomBytes + pos[g & 1];
+                const uint4 lo = *reinterpret_cast<const uint4*>(r0 + at);
+                const uint4 hi = *reinterpret_cast<const uint4*>(r1 + at);
                 const uint4* bp = b + ((first + j) * 4 + g) * NT * 32 + lane;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -459,21 +685,24 @@ __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, con
 #pragma unroll
                 for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // 64 elements each
-                const uint4 lo = *reinterpret_cast<const uint4*>(r0 + j * 128 + g * 64);
-                const uint4 hi = *reinterpret_cast<const uint4*>(r1 + j * 128 + g * 64);
+            for (int g = 0; g < 2; ++g) {  // 64 elements each, 1 atom
+                const int at = j * kAtomBytes + pos[g];
+                const uint4 lo = *reinterpret_cast<const uint4*>(r0 + at);
+                const uint4 hi = *reinterpret_cast<const uint4*>(r1 + at);
                 const uint32_t l4[4] = {lo.x, lo.y, lo.z, lo.w}, h4[4] = {hi.x, hi.y, hi.z, hi.w};
                 const uint4* bp = b + ((first + j) * 2 + g) * 2 * NT * 32 + lane;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t a0, a1, a2, a3;
-                    widen(l4[q], a0, a2);
-                    widen(h4[q], a1, a3);
+                for (int q = 0; q < 4; q += 2) {
+                    uint32_t a[8];
+                    widen(l4[q], a[0], a[2]);
+                    widen(h4[q], a[1], a[3]);
+                    widen(l4[q + 1], a[4], a[6]);
+                    widen(h4[q + 1], a[5], a[7]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const uint2 v = reinterpret_cast<const uint2*>(
-                            bp + ((q >> 1) * NT + n) * 32)[q & 1];
-                        mma16816(part[n], a0, a1, a2, a3, v.x, v.y);
+                        const uint4 v = bp[((q >> 1) * NT + n) * 32];
+                        mma16816_f16(part[n], a[0], a[1], a[2], a[3], v.x, v.y);
+                        mma16816_f16(part[n], a[4], a[5], a[6], a[7], v.z, v.w);
                     }
                 }
             }
@@ -489,7 +718,7 @@ __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, con
     }
 }
 
-// All consumer warps meet (bounded, unlike bar.sync: a warp that gave up does
+// All product warps meet (bounded, unlike bar.sync: a warp that gave up does
 // not come).
 __device__ __forceinline__ bool warps_meet(const FewArgs& a, const Smem& s, int lane,
                                            int& parity) {
@@ -502,74 +731,91 @@ __device__ __forceinline__ bool warps_meet(const FewArgs& a, const Smem& s, int 
 }
 
 template <int NT, bool FP8>
-__device__ __forceinline__ void consumer(const FewArgs& a, const Smem& s, int warp, int lane) {
+__device__ __forceinline__ void products(const FewArgs& a, const Smem& s, int warp, int lane) {
     constexpr int esz = FP8 ? 1 : 2;
     const int tid = warp * 32 + lane;
-    const int T = a.T, d = a.d, E = a.E, k = a.k, I = a.I, S = a.S;
-    const uint32_t all = T >= 32 ? 0xffffffffu : (1u << T) - 1u;
+    const int T = a.T, d = a.d, I = a.I, S = a.S;
+    const uint32_t all = (1u << T) - 1u;
     // ---- x as operand B
-    fill_b<NT, FP8>(s.b, a.x, d, d, all, 8 * NT, true, tid);
-    for (int e = tid; e < E; e += 32 * kWarps) s.s_mask[e] = 0;
-    // ---- routing: every CTA chooses for itself, CTA 0 writes it out
-    pdl_wait();
-    float* lg = reinterpret_cast<float*>(s.red);
-    for (int i = tid; i < T * E; i += 32 * kWarps) lg[i] = __ldcg(a.logits + i);
-    consumers_sync();
-    for (int t = warp; t < T; t += kWarps) {
-        warp_topk<kMaxE / 32>(lg + t * E, lane, E, k, a.G, a.TG, a.gate, a.bias, s.s_idx + t * k,
-                              s.s_w + t * k);
-        __syncwarp();
-        if (lane < k) {
-            atomicOr(s.s_mask + s.s_idx[t * k + lane], 1u << t);
-            if (blockIdx.x == 0) {
-                if (a.idx_out != nullptr) a.idx_out[t * k + lane] = s.s_idx[t * k + lane];
-                if (a.w_out != nullptr) a.w_out[t * k + lane] = s.s_w[t * k + lane];
-            }
-        }
-    }
-    consumers_sync();
-    if (warp == 0) {
-        int n = S;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            const bool on = e < E && s.s_mask[e] != 0;
-            const uint32_t vote = __ballot_sync(0xffffffffu, on);
-            if (on) s.list[n + __popc(vote & ((1u << lane) - 1u))] = e;
-            n += __popc(vote);
-        }
-        if (lane == 0) *s.n_entries = n;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s.routed);
-    }
-    consumers_sync();
-    const int n_entries = *s.n_entries;
+    fill_b<NT, FP8>(s, a.x, d, d, all, 8 * NT, true, warp, lane);
+    products_sync();
 
     // ---- units
     const Pieces pu = pieces(d, esz), pd = pieces(I, esz);
     float acc[NT][4];
     int slot = 0, phase = 0;
-    int unit = 0;          // finished units: whose turn it is, and which buffer
+    int unit = 0;          // units so far
     int have = -1;         // entry whose h is operand B
     int parity = 0;
+    float un[NT][2];       // 8-bit weights: unscale of this lane's two tokens per column group
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            un[n][q] = FP8 && 8 * n + 2 * (lane & 3) + q < T
+                           ? s.unscale[8 * n + 2 * (lane & 3) + q] : 1.f;
+    // the unit and this warp's partial sums, to the sum warp whose turn it is
+    auto hand_over = [&](const int4& info, bool data) {
+        const int buf = unit % kSumBufs, who = unit % kSumWarps;
+        const bool ok = mbar_wait_bounded(s.sum_empty + buf, ((unit / kSumBufs) & 1) ^ 1, s.abort,
+                                          a.status, SITE_GEMM_EPILOGUE, a.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (data) {
+            float4* red = s.red + buf * kWarps * NT * 32;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                red[(warp * NT + n) * 32 + lane] =
+                    make_float4(acc[n][0] * un[n][0], acc[n][1] * un[n][1], acc[n][2] * un[n][0],
+                                acc[n][3] * un[n][1]);
+        }
+        if (tid == 0) s.unit[who] = info;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.sum_full + who);
+        ++unit;
+        return true;
+    };
     for (;;) {
         const bool filled = mbar_wait_bounded(s.full + slot, phase, s.abort, a.status,
                                               SITE_GEMM_MMA, a.wait_limit_ns);
         if (!__all_sync(0xffffffffu, filled)) return;
         const int4 info = s.info[slot];
-        if (info.x < 0) return;
-        const bool up = info.x == 1;
-        const int entry = info.y, tile = info.z, c = info.w;
+        if (info.x == WHAT_END || info.x == WHAT_TOLD || info.x == WHAT_Y) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s.empty + slot);
+            if (++slot == a.stages) {
+                slot = 0;
+                phase ^= 1;
+            }
+            // y goes to one sum warp, the others concern them all
+            for (int i = 0; i < (info.x == WHAT_Y ? 1 : kSumWarps); ++i)
+                if (!hand_over(info, false)) return;
+            if (info.x == WHAT_END) return;
+            continue;
+        }
+        const bool up = info.x == WHAT_UP;
+        const int entry = info.y, c = info.w;
         const Pieces p = up ? pu : pd;
         const int K = up ? d : I;
-        const uint32_t mask = entry < S ? all : s.s_mask[s.list[entry]];
         if (!up && have != entry) {
-            // every warp is past the last unit's products (they met after it)
-            bool ok = wait_count(a.ctrl + kCtrlH + entry, I / 8, s.abort, a.status,
-                                 SITE_GEMM_BOUNDS, a.wait_limit_ns);
+            // the last products with the old operand are done, and h is there
+            if (!warps_meet(a, s, lane, parity)) return;
+            bool ok = mbar_wait_bounded(s.routed, 0, s.abort, a.status, SITE_GEMM_EPILOGUE,
+                                        a.wait_limit_ns);  // the entry list: long there
+            ok = ok && wait_count(a.ctrl + kCtrlH + entry, I / 8, s.abort, a.status,
+                                       SITE_GEMM_BOUNDS, a.wait_limit_ns);
             if (!__all_sync(0xffffffffu, ok)) return;
-            fill_b<NT, FP8>(s.b, a.h + (size_t)entry * T * I, I, I, mask, T, false, tid);
+            const uint32_t mask = entry < S ? all : s.s_mask[s.list[entry]];
+            fill_b<NT, FP8>(s, a.h + (size_t)entry * T * I, I, I, mask, T, false, warp, lane);
             have = entry;
             if (!warps_meet(a, s, lane, parity)) return;
+            if (FP8) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (8 * n + 2 * (lane & 3) + q < T)
+                            un[n][q] = s.unscale[8 * n + 2 * (lane & 3) + q];
+            }
         }
         if (c == 0) {
 #pragma unroll
@@ -587,92 +833,167 @@ __device__ __forceinline__ void consumer(const FewArgs& a, const Smem& s, int wa
             phase ^= 1;
         }
         if (c + 1 < p.n) continue;
-        // ---- the unit's sums
-        float4* red = s.red + (unit & 1) * kWarps * NT * 32;
+        if (!hand_over(info, true)) return;
+    }
+}
+
+// ---------------------------------------------------------------- sums
+template <int NT>
+__device__ __forceinline__ void sums(const FewArgs& a, const Smem& s, int who, int lane) {
+    const int T = a.T, d = a.d, E = a.E, k = a.k, I = a.I, S = a.S;
+    const uint32_t all = (1u << T) - 1u;
+    // ---- routing: every CTA chooses for itself, CTA 0 writes it out
+    const int tid = who * 32 + lane;
+    for (int e = tid; e < E; e += 32 * kSumWarps) s.s_mask[e] = 0;
+    pdl_wait();
+    for (int i = tid; i < T * E; i += 32 * kSumWarps)
+        s.keys[i] = __float_as_uint(__ldcg(a.logits + i));
+    sums_sync();
+    for (int t = who; t < T; t += kSumWarps) {
+        choose(s.keys + t * E, lane, E, k, a.G, a.TG, a.gate, a.bias, s.s_idx + t * k,
+               s.s_w + t * k);
+        __syncwarp();
+        if (lane < k) {
+            atomicOr(s.s_mask + s.s_idx[t * k + lane], 1u << t);
+            if (blockIdx.x == 0) {
+                if (a.idx_out != nullptr) a.idx_out[t * k + lane] = s.s_idx[t * k + lane];
+                if (a.w_out != nullptr) a.w_out[t * k + lane] = s.s_w[t * k + lane];
+            }
+        }
+    }
+    sums_sync();
+    if (who == 0) {
+        int n = S;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            const bool on = e < E && s.s_mask[e] != 0;
+            const uint32_t vote = __ballot_sync(0xffffffffu, on);
+            if (on) s.list[n + __popc(vote & ((1u << lane) - 1u))] = e;
+            n += __popc(vote);
+        }
+        if (lane == 0) *s.n_entries = n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.routed);
+    }
+    sums_sync();
+
+    // ---- units
+    int told_entry = 0, untold = 0;  // gate/up units stored and not told yet
+    auto tell = [&]() {
+        __syncwarp();
+        if (lane == 0 && untold > 0) {
+            __threadfence();
+            atomicAdd(a.ctrl + kCtrlH + told_entry, untold);
+        }
+        untold = 0;
+    };
+    for (int unit = who;; unit += kSumWarps) {
+        const bool filled = mbar_wait_bounded(s.sum_full + who, (unit / kSumWarps) & 1, s.abort,
+                                              a.status, SITE_GEMM_EPILOGUE, a.wait_limit_ns);
+        if (!__all_sync(0xffffffffu, filled)) return;
+        const int4 info = s.unit[who];
+        const int buf = unit % kSumBufs;
+        const float4* red = s.red + buf * kWarps * NT * 32 + lane;
+        float4 sum[NT];
+        if (info.x == WHAT_UP || info.x == WHAT_DOWN) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            red[(warp * NT + n) * 32 + lane] =
-                make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-        if (!warps_meet(a, s, lane, parity)) return;
-        const bool mine = (unit & 7) == warp;
-        ++unit;
-        if (!mine) continue;
+            for (int n = 0; n < NT; ++n) {
+                float4 v = red[n * 32];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 o = red[(w * NT + n) * 32];
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                sum[n] = v;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.sum_empty + buf);
+        if (info.x == WHAT_END) return;
+        if (info.x == WHAT_TOLD) {
+            tell();
+            if (info.y == PART_DOWN && lane == 0) {
+                __threadfence();
+                atomicAdd(a.ctrl + kCtrlDown, 1);
+            }
+            continue;
+        }
+        const int entry = info.y, tile = info.z;
+        if (info.x == WHAT_Y) {
+            // ---- 16 columns of y: the slots of each token in order, once every
+            // sum warp of every down run has told
+            const bool ok = wait_count(a.ctrl + kCtrlDown, kSumWarps * (int)gridDim.x, s.abort,
+                                       a.status, SITE_GEMM_BOUNDS, a.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            for (int i = lane; i < T * 4; i += 32) {
+                const int t = i >> 2, col = tile * 16 + (i & 3) * 4;
+                const float* src = a.slots + (size_t)t * (S + k) * d + col;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int j = 0; j < S + k; ++j) {
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(src + (size_t)j * d));
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                if (a.out_f32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + (size_t)t * d + col) = v;
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + (size_t)t * d +
+                                              col) =
+                        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            }
+            continue;
+        }
+        const bool up = info.x == WHAT_UP;
+        const int expert = entry < S ? -1 : s.list[entry];
+        const uint32_t mask = expert < 0 ? all : s.s_mask[expert];
+        if (up) {
+            if (entry != told_entry) tell();
+            told_entry = entry;
+            ++untold;
+        }
+        const int g = lane >> 2;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float4 v = red[n * 32 + lane];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const float4 o = red[(w * NT + n) * 32 + lane];
-                v.x += o.x;
-                v.y += o.y;
-                v.z += o.z;
-                v.w += o.w;
-            }
-            const int g = lane >> 2;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int t = 8 * n + 2 * (lane & 3) + q;
-                if (t >= T || !((mask >> t) & 1u)) continue;
-                const float s0 = q ? v.y : v.x, s1 = q ? v.w : v.z;  // rows g and g + 8
+                if (!((mask >> t) & 1u)) continue;
+                // rows g and g + 8 of the unit
+                const float s0 = q ? sum[n].y : sum[n].x, s1 = q ? sum[n].w : sum[n].z;
                 if (up) {
                     const float h = s0 / (1.f + expf(-s0)) * s1;
                     a.h[((size_t)entry * T + t) * I + tile * 8 + g] = __float2bfloat16_rn(h);
                 } else {
                     int j = entry;
                     float wt = 1.f;
-                    if (entry >= S) {
-                        const int e = s.list[entry];
+                    if (expert >= 0)
                         for (int i = 0; i < k; ++i)
-                            if (s.s_idx[t * k + i] == e) {
+                            if (s.s_idx[t * k + i] == expert) {
                                 j = S + i;
                                 wt = s.s_w[t * k + i];
                             }
-                    }
                     float* o = a.slots + ((size_t)t * (S + k) + j) * d + tile * 16 + g;
                     __stcg(o, wt * s0);
                     __stcg(o + 8, wt * s1);
                 }
             }
         }
-        __syncwarp();
-        int last = 0;
-        if (lane == 0) {
-            __threadfence();
-            if (up)
-                atomicAdd(a.ctrl + kCtrlH + entry, 1);
-            else
-                last = atomicAdd(a.ctrl + kCtrlY + tile, 1) == n_entries - 1;
-            __threadfence();
-        }
-        last = __shfl_sync(0xffffffffu, last, 0);
-        __syncwarp();  // lane 0's fence comes before the other lanes' reads
-        if (!last) continue;
-        // ---- y of these 16 columns: the slots of each token in order
-        for (int i = lane; i < T * 4; i += 32) {
-            const int t = i >> 2, col = tile * 16 + (i & 3) * 4;
-            const float* src = a.slots + (size_t)t * (S + k) * d + col;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int j = 0; j < S + k; ++j) {
-                const float4 o = __ldcg(reinterpret_cast<const float4*>(src + (size_t)j * d));
-                v.x += o.x;
-                v.y += o.y;
-                v.z += o.z;
-                v.w += o.w;
-            }
-            if (a.out_f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(a.y) + (size_t)t * d + col) = v;
-            else
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + (size_t)t * d + col) =
-                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        }
     }
 }
 
 template <int NT, bool FP8>
-__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewArgs a) {
-    extern __shared__ __align__(1024) uint8_t few_smem[];
-    const Smem s = carve<NT>(few_smem, a.stages, a.d, a.I);
+__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_constant__ FewArgs a) {
+    extern __shared__ uint8_t few_smem[];
+    // swizzled stages start at multiples of 1024 bytes
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem) + 1023) &
+                                               ~(uintptr_t)1023);
+    const Smem s = carve<NT>(base, a.stages, a.d, a.I);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -681,14 +1002,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewArgs
         }
         mbar_init(s.routed, 1);
         mbar_init(s.meet, kWarps);
+        for (int i = 0; i < kSumWarps; ++i) mbar_init(s.sum_full + i, kWarps);
+        for (int i = 0; i < kSumBufs; ++i) mbar_init(s.sum_empty + i, 1);
         *s.abort = 0;
         fence_barrier_init();
     }
     __syncthreads();
-    if (warp == kWarps)
-        producer<FP8>(a, s, lane);
+    if (warp < kWarps)
+        products<NT, FP8>(a, s, warp, lane);
+    else if (warp < kWarps + kSumWarps)
+        sums<NT>(a, s, warp - kWarps, lane);
     else
-        consumer<NT, FP8>(a, s, warp, lane);
+        producer<FP8>(a, s, lane);
     __syncthreads();
     pdl_trigger();
 }
@@ -696,10 +1021,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewArgs
 // ---------------------------------------------------------------- host
 enum FewRegion : int { FW_STATUS, FW_CTRL, FW_LOGITS, FW_H, FW_SLOTS, FW_TOTAL };
 
-int few_stages(int T, int d, int I) {
+int few_stages(int T, int d, int E, int I) {
     const int nt = T > 8 ? 2 : 1;
     const long long fixed = (long long)8 * nt * 2 * (d > I ? d : I) +
-                            (nt == 1 ? red_bytes<1>() : red_bytes<2>()) + kSmallBytes;
+                            (nt == 1 ? red_bytes<1>() : red_bytes<2>()) + kSmallBytes +
+                            4 * T * E;
     const long long n = (kSmemMax - fixed) / kStageBytes;
     return n < 2 ? 0 : (int)std::min<long long>(n, kMaxStages);
 }
@@ -709,7 +1035,7 @@ int few_check(int T, int d, int E, int k, int inter, int n_shared) {
         n_shared < 0)
         return MOE_ERR_INVALID_ARG;
     if (d % 256 != 0 || inter % 128 != 0 || n_shared > kMaxShared || T > kFewMaxT ||
-        (long long)n_shared * inter > INT_MAX / 2 || few_stages(T, d, inter) == 0)
+        (long long)n_shared * inter > INT_MAX / 2 || few_stages(T, d, E, inter) == 0)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -717,7 +1043,7 @@ int few_check(int T, int d, int E, int k, int inter, int n_shared) {
 bool few_layout(int T, int d, int E, int k, int inter, int n_shared, size_t (&off)[FW_TOTAL + 1]) {
     if (few_check(T, d, E, k, inter, n_shared) != MOE_OK) return false;
     const size_t entries = (size_t)n_shared + std::min(E, T * k);
-    const size_t sizes[FW_TOTAL] = {sizeof(int) * kStatusWords, sizeof(int) * (kCtrlY + d / 16),
+    const size_t sizes[FW_TOTAL] = {sizeof(int) * kStatusWords, sizeof(int) * kCtrlWords,
                                     sizeof(float) * T * E, 2 * entries * T * inter,
                                     sizeof(float) * T * (n_shared + k) * (size_t)d};
     size_t o = 0;
@@ -732,7 +1058,8 @@ bool few_layout(int T, int d, int E, int k, int inter, int n_shared, size_t (&of
 template <int NT, bool FP8>
 cudaError_t launch_layer(const FewArgs& a, cudaStream_t s) {
     auto kern = few_layer_kernel<NT, FP8>;
-    const int smem = a.stages * kStageBytes + b_bytes<NT>(a.d, a.I) + red_bytes<NT>() + kSmallBytes;
+    const int smem = a.stages * kStageBytes + b_bytes<NT>(a.d, a.I) + red_bytes<NT>() + kSmallBytes +
+                     4 * a.T * a.E;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)num_sms()), dim3(kFewThreads), (size_t)smem, s, 1, a);
@@ -792,10 +1119,19 @@ MOE_API int moe_forward_few(const void* x, const void* W_router, const void* W_g
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     FewArgs a{};
+    const int esz = fp8 ? 1 : 2;
+    const Pieces pu = pieces(d, esz), pd = pieces(inter, esz);
+    const uint64_t SI = (uint64_t)n_shared * inter;
+    const uint32_t au = (uint32_t)(pu.len * esz / 128), ad = (uint32_t)(pd.len * esz / 128);
+    const char* sh = static_cast<const char*>(W_shared);
+    if (!make_map_atoms16(&a.up_map[1], W_gate_up, (uint64_t)E * 2 * inter, (uint64_t)d * esz,
+                          inter, au) ||
+        !make_map_atoms16(&a.down_map[1], W_down, (uint64_t)E * d, (uint64_t)inter * esz, 0, ad) ||
+        (n_shared > 0 &&
+         (!make_map_atoms16(&a.up_map[0], sh, 2 * SI, (uint64_t)d * esz, SI, au) ||
+          !make_map_atoms16(&a.down_map[0], sh + 2 * SI * d * esz, (uint64_t)d, SI * esz, 0, ad))))
+        return MOE_ERR_CUDA;
     a.x = static_cast<const __nv_bfloat16*>(x);
-    a.w_gate_up = W_gate_up;
-    a.w_down = W_down;
-    a.w_shared = W_shared;
     a.s_gate_up = s_gate_up;
     a.s_down = s_down;
     a.s_shared = s_shared;
@@ -811,8 +1147,7 @@ MOE_API int moe_forward_few(const void* x, const void* W_router, const void* W_g
     a.I = inter;
     a.S = n_shared;
     a.out_f32 = out_dt == MOE_F32;
-    a.stages = few_stages(T, d, inter);
-    a.tile_rows = 2;
+    a.stages = few_stages(T, d, E, inter);
     a.y = y;
     a.idx_out = topk_idx_out;
     a.w_out = topk_w_out;
@@ -821,10 +1156,16 @@ MOE_API int moe_forward_few(const void* x, const void* W_router, const void* W_g
     a.h = reinterpret_cast<__nv_bfloat16*>(ws + off[FW_H]);
     a.slots = reinterpret_cast<float*>(ws + off[FW_SLOTS]);
     a.wait_limit_ns = kWaitLimitNs;
-    cudaError_t e = launch_pdl(few_logits_kernel, dim3((unsigned)E), dim3(kLogitThreads), 0, s, 1,
+    // the layer kernel needs all of an SM's shared memory: an SM that runs the
+    // logits kernel with another split could not take it before that ends
+    cudaError_t e = cudaFuncSetAttribute(few_logits_kernel,
+                                         cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    e = launch_pdl(few_logits_kernel, dim3((unsigned)E), dim3(kLogitThreads), 0, s, 1,
                                a.x, static_cast<const __nv_bfloat16*>(W_router), T, d, E,
                                reinterpret_cast<float*>(ws + off[FW_LOGITS]), a.status, a.ctrl,
-                               kCtrlY + d / 16);
+                               kCtrlWords);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (fp8) return ret(T > 8 ? launch_layer<2, true>(a, s) : launch_layer<1, true>(a, s));
     return ret(T > 8 ? launch_layer<2, false>(a, s) : launch_layer<1, false>(a, s));

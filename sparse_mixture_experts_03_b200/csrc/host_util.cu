@@ -106,6 +106,35 @@ bool make_map_gate_up(CUtensorMap* m, const void* base, uint64_t G, uint64_t F, 
     return r == CUDA_SUCCESS;
 }
 
+// Rows of row_bytes bytes (a multiple of 128) as 128-byte atoms: one box brings
+// 16 rows x atoms x 128 bytes as [atom][16 rows][128 B], 128B-swizzled.  half_rows
+// == 0: {128 B, rows, atoms}, 16 neighbouring rows.  Else {128 B, rows -
+// half_rows, 2, atoms}: 8 rows and the 8 rows half_rows further on (gate and up
+// rows of the same features).
+bool make_map_atoms16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes,
+                      uint64_t half_rows, uint32_t atoms) {
+    auto fn = encode_fn();
+    if (fn == nullptr || row_bytes % 128 != 0 || rows <= half_rows || atoms == 0) return false;
+    CUresult r;
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (half_rows == 0) {
+        cuuint64_t dims[3] = {128, rows, row_bytes / 128};
+        cuuint64_t strides[2] = {row_bytes, 128};
+        cuuint32_t box[3] = {128, 16, atoms};
+        r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        cuuint64_t dims[4] = {128, rows - half_rows, 2, row_bytes / 128};
+        cuuint64_t strides[3] = {row_bytes, half_rows * row_bytes, 128};
+        cuuint32_t box[4] = {128, 8, 2, atoms};
+        r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    return r == CUDA_SUCCESS;
+}
+
 // e4m3 matrices [G][rows][K] as {K, rows, G}: one box {128, box_rows, 1} brings
 // box_rows rows x 128 of K as one 128B-swizzled tile; K % 16 == 0, what lies
 // behind K, the rows or G reads as zeros.  three_d false: the first matrix alone, as {K, rows}.

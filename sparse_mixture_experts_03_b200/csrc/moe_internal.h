@@ -260,6 +260,11 @@ bool make_map_rows_atoms(CUtensorMap* m, const void* base, uint64_t rows, uint64
                          uint32_t box_rows = 128);
 bool make_token_maps(CUtensorMap (&m)[kTokenBoxes], const void* base, uint64_t rows, uint64_t K);
 bool make_map_gate_up(CUtensorMap* m, const void* base, uint64_t G, uint64_t F, uint64_t K);
+// Rows of row_bytes bytes as boxes of 16 rows x atoms x 128 bytes ([atom][16
+// rows][128 B], 128-byte swizzle): 16 neighbouring rows, or with half_rows 8 rows
+// and the 8 rows half_rows further on.
+bool make_map_atoms16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes,
+                      uint64_t half_rows, uint32_t atoms);
 // 8-bit (e4m3) matrices [G][rows][K] as {K, rows, G} (three_d) or {K, rows}:
 // boxes of box_rows rows x 128 of K, 128-byte swizzle.
 bool make_map_e4m3(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t G,
