@@ -23,7 +23,7 @@
 //       of A, read from the stage as 16 bytes per lane, the tokens the 8
 //       columns of B.  The tensor work is a few percent of what the SM can do;
 //       tcgen05 tiles of 128 rows would only make the units coarser.
-//     - 4 sum warps take the units in turn and add their 8 partial sums in warp
+//     - 4 sum warps take the units in turn and add their partial sums in warp
 //       order; gate and up rows of a feature meet in one lane, h = silu(g) u is
 //       rounded once to bf16 (the operand type of the down product).  Down
 //       sums go, times the gate weight, into fp32 slots [token][S + k][d]; y adds
@@ -35,14 +35,18 @@
 //       T = 1 take 83 us and T = 16 432 us; per unit but by the sum warps 65
 //       and 322.)
 //   The units of each part (shared up, routed up, down, y) are cut into gridDim.x
-//   runs of neighbours; a CTA takes a run by a ticket, one atomic per part.
+//   runs of neighbours.  CTA b claims run b of each part (ahead of time, so that
+//   nothing waits for the answer) and, at its end, any run that a CTA which is
+//   not on the GPU yet has left.  Its first run's loads do not wait for the claim
+//   or the logits: were the run another's by then, it would store the same h
+//   again and not count it.
 //
-// Results do not depend on which CTA took which ticket: every unit is summed
+// Results do not depend on which CTA took which run: every unit is summed
 // the same way wherever it runs, and the slots are added in order.
 //
 // Waits between CTAs (down units wait for the h of their expert) cannot
 // deadlock whatever else runs on the GPU: a CTA goes to the next part when all
-// runs of this one are taken, so all that a run waits for is in the hands of
+// runs of this one are claimed, so all that a run waits for is in the hands of
 // CTAs that already run, and they do it before they wait for anything later.
 // All waits are bounded.
 //
@@ -54,8 +58,11 @@
 // times a power of two that brings its largest magnitude to [2^14, 2^15).
 // bf16's 8 bits fit fp16's 11 down to 2^-28 of the largest magnitude, and what
 // lies below is off by at most 2^-39 of it, far less than the fp32 sums are.
+// What bounds the 8-bit layer is this conversion (it runs at 16 codes a clock
+// and SM, 0.55 us a stage that arrives in 0.73).  Not faster: shifts and masks
+// instead (90 us against 80 at T = 5), half and half (87), 16 product warps
+// (82), and m16n8k32 on the codes with the tokens as two e4m3 terms (86).
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <limits.h>
 
 #include <algorithm>
@@ -72,10 +79,14 @@ constexpr int kSumWarps = 4;
 constexpr int kSumBufs = 2;                     // partial sums in flight (a sum warp frees its
                                                 // buffer before it stores and tells)
 constexpr int kFewThreads = 32 * (kWarps + kSumWarps + 1);  // + the producer warp
-constexpr int kRowBytes = 2048;                 // bytes of one weight row in a stage
 constexpr int kAtomBytes = 16 * 128;            // 16 rows x 128 bytes
-constexpr int kStageBytes = 16 * kRowBytes;     // [atom][16 rows][128 bytes]
+// Atoms of a stage.  Half as many made 16 tokens 20% slower (1 KB of a row at a
+// time instead of 2).
+constexpr int kStageAtoms = 16;
+constexpr int kStageBytes = kStageAtoms * kAtomBytes;
 constexpr int kMaxStages = 6;
+constexpr int kMinRing = 64 * 1024;
+constexpr int kMaxGrid = 256;
 constexpr int kMaxShared = 64;                  // shared experts
 constexpr int kMaxEntries = kMaxShared + kFewMaxT * kMaxK;
 constexpr int kSmemMax = 227 * 1024;
@@ -90,11 +101,10 @@ enum What : int {
     WHAT_TOLD = 2,  // the end of a run: tell the other CTAs
     WHAT_Y = 3,     // 16 columns of y
 };
-// Control words (reset by few_logits_kernel), each counter on a sector of its
-// own: the tickets of each part, the sum warps that finished a down run, finished
-// gate/up units per entry.
-constexpr int kCtrlTicket = 0;  // + 8 * part
-constexpr int kCtrlDown = 8 * kParts;
+// Control words (reset by few_logits_kernel): the claims of each part's runs,
+// the sum warps that finished a down run, finished gate/up units per entry.
+constexpr int kCtrlClaim = 0;  // + kMaxGrid * part
+constexpr int kCtrlDown = kMaxGrid * kParts;
 constexpr int kCtrlH = kCtrlDown + 8;
 constexpr int kCtrlWords = kCtrlH + kMaxEntries;
 
@@ -163,32 +173,40 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 
 // The k experts of one token and their weights, by one warp: the rules of the
 // router kernels (largest keys inside the topk_group groups of largest maximum,
-// ties to the lower index), as short loops: this code runs once per launch and
-// its instructions come from L2, so its length is its time.  key [E] is scratch
-// and starts as the logits.
-__device__ __noinline__ void choose(uint32_t* key, int lane, int E, int k, int G, int TG, int gate,
-                                    const float* bias, int* idx, float* w) {
+// ties to the lower index).  Lane l holds experts l EJ ..; a round is a warp
+// maximum and a vote.  The code runs once per launch and its instructions come
+// from L2, so the loops over choices stay loops.  key [E] is scratch.
+template <int EJ>
+__device__ __forceinline__ void choose(const float* logit, uint32_t* key, int lane, int E, int k,
+                                       int G, int TG, int gate, const float* bias, int* idx,
+                                       float* w) {
     const int gsz = E / G;
-    float* logit = reinterpret_cast<float*>(key);
-    // the token's logits stay in registers of the lanes for the weights
-    float mine[kMaxE / 32];
+    float mine[EJ];
+    uint32_t mk[EJ];
 #pragma unroll
-    for (int j = 0; j < kMaxE / 32; ++j) {
-        const int e = lane + 32 * j;
-        mine[j] = 0.f;
+    for (int j = 0; j < EJ; ++j) {
+        const int e = lane * EJ + j;
+        mine[j] = e < E ? __ldcg(logit + e) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < EJ; ++j) {
+        const int e = lane * EJ + j;
+        mk[j] = 0;  // ordered() never gives 0: it marks what is out
         if (e < E) {
-            const float l = logit[e];
-            mine[j] = l;
             // the gate score is monotone in the logit: without a bias the logit is the key
-            const float g = bias == nullptr ? l
-                            : (gate == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-l)) : l) + bias[e];
-            key[e] = ordered(g);
+            float g = mine[j];
+            if (bias != nullptr)
+                g = (gate == MOE_GATE_SIGMOID ? 1.f / (1.f + expf(-g)) : g) + bias[e];
+            mk[j] = ordered(g);
+            key[e] = mk[j];
         }
     }
     __syncwarp();
-    uint32_t best = 0;  // ordered() never gives 0: it marks what is out
-    if (lane < G)
-        for (int e = lane * gsz; e < (lane + 1) * gsz; ++e) best = max(best, key[e]);
+    uint32_t best = 0;
+    if (lane < G) {
+#pragma unroll 4
+        for (int i = 0; i < gsz; ++i) best = max(best, key[lane * gsz + i]);
+    }
     uint32_t kept = 0;
 #pragma unroll 1
     for (int r = 0; r < TG; ++r) {
@@ -197,44 +215,48 @@ __device__ __noinline__ void choose(uint32_t* key, int lane, int E, int k, int G
         kept |= 1u << g;
         if (lane == g) best = 0;
     }
-    for (int e = lane; e < E; e += 32)
-        if (!((kept >> (e / gsz)) & 1u)) key[e] = 0;
+#pragma unroll
+    for (int j = 0; j < EJ; ++j)
+        if (!((kept >> ((unsigned)min(lane * EJ + j, E - 1) / (unsigned)gsz)) & 1u)) mk[j] = 0;
     float l = 0.f;  // lane r: the r-th choice's logit
 #pragma unroll 1
     for (int r = 0; r < k; ++r) {
-        __syncwarp();
-        uint32_t b = 0;
-        int be = kMaxE;
-        for (int e = lane; e < E; e += 32)
-            if (key[e] > b) {
-                b = key[e];
-                be = e;
+        uint32_t b = mk[0];
+        int bj = 0;
+        float bl = mine[0];
+#pragma unroll
+        for (int j = 1; j < EJ; ++j)
+            if (mk[j] > b) {
+                b = mk[j];
+                bj = j;
+                bl = mine[j];
             }
         const uint32_t top = __reduce_max_sync(0xffffffffu, b);
-        const int e = (int)__reduce_min_sync(0xffffffffu, b == top ? (uint32_t)be : (uint32_t)kMaxE);
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < kMaxE / 32; ++j)
-            if (j == e >> 5) v = mine[j];
-        v = __shfl_sync(0xffffffffu, v, e & 31);
+        const int src = __ffs(__ballot_sync(0xffffffffu, b == top)) - 1;
+        const int e = src * EJ + __shfl_sync(0xffffffffu, bj, src);
+        const float v = __shfl_sync(0xffffffffu, bl, src);
         if (lane == r) {
             l = v;
             idx[r] = e;
         }
-        if (lane == (e & 31)) key[e] = 0;
+        if (lane == src) {
+#pragma unroll
+            for (int j = 0; j < EJ; ++j)
+                if (j == bj) mk[j] = 0;
+        }
     }
     // weights in the router kernels' order of operations
-    float s = 0.f;
+    float sc;
     if (gate == MOE_GATE_SIGMOID) {
-        s = 1.f / (1.f + expf(-l));
+        sc = 1.f / (1.f + expf(-l));
     } else {
         float m = __shfl_sync(0xffffffffu, l, 0);
         for (int r = 1; r < k; ++r) m = fmaxf(m, __shfl_sync(0xffffffffu, l, r));
-        s = expf(l - m);
+        sc = expf(l - m);
     }
     float sum = 0.f;
-    for (int r = 0; r < k; ++r) sum += __shfl_sync(0xffffffffu, s, r);
-    if (lane < k) w[lane] = s / sum;
+    for (int r = 0; r < k; ++r) sum += __shfl_sync(0xffffffffu, sc, r);
+    if (lane < k) w[lane] = sc / sum;
 }
 
 // ---------------------------------------------------------------- copies
@@ -254,12 +276,6 @@ __device__ __forceinline__ void box_4d(void* dst, const CUtensorMap* map, uint64
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(atom)
         : "memory");
 }
-__device__ __forceinline__ void box_4d_to_l2(const CUtensorMap* map, int row, int atom) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %1, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(0), "r"(row), "r"(atom)
-                 : "memory");
-}
 __device__ __forceinline__ void copy_scale(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
                  : "memory");
@@ -278,7 +294,7 @@ __device__ __forceinline__ void sums_sync() {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -286,7 +302,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 __device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -309,13 +325,16 @@ __device__ __forceinline__ void widen(uint32_t codes, uint32_t& lo, uint32_t& hi
 struct Smem {
     uint8_t* ring;
     uint4* b;        // operand B: x (gate/up units), then the h of one entry
-    float4* red;     // [kSumBufs][kWarps][NT][32]
+    float4* red;     // [kSumBufs][product warps][NT][32]
     float* scales;   // [stages][32]
     int4* info;      // [stages]
     uint64_t* full;
     uint64_t* empty;
     uint64_t* routed;  // the entry list is there
-    uint32_t* keys;    // [T][E] logits, then selection keys
+    uint32_t* keys;    // [kSumWarps][E] selection keys
+    uint64_t* claimed; // the claims of this CTA's first runs are answered:
+    int* first_mine;   // 1: the first shared run is its own
+    int* ahead;        // 0: so is the routed one
     uint64_t* meet;    // the product warps, around a new operand B
     uint64_t* sum_full;   // [kSumWarps]: a unit's partial sums are there
     uint64_t* sum_empty;  // [kSumBufs]
@@ -335,7 +354,7 @@ __host__ __device__ constexpr int red_bytes() {
 }
 constexpr int kSmallBytes = 1024 + kMaxStages * (32 * 4 + 16 + 16) + 64 + kSumWarps * 24 + kSumBufs * 8 +
                             kFewMaxT * 4 + kFewMaxT * kMaxK * 8 + kMaxE * 4 + kMaxEntries * 4 +
-                            64;
+                            kSumWarps * kMaxE * 4 + 64;
 
 template <int NT>
 __host__ __device__ inline int b_bytes(int d, int I) {
@@ -380,12 +399,14 @@ __device__ __forceinline__ Smem carve(uint8_t* p, int stages, int d, int I) {
     p += kMaxEntries * 4;
     s.n_entries = reinterpret_cast<int*>(p);
     s.abort = s.n_entries + 1;
+    s.first_mine = s.n_entries + 2;
+    s.ahead = s.n_entries + 3;
+    p += 16;
+    s.claimed = reinterpret_cast<uint64_t*>(p);
     p += 16;
     s.keys = reinterpret_cast<uint32_t*>(p);
     return s;
 }
-
-constexpr int kAhead = 4;  // units that are on their way to L2 ahead of the ring
 
 // Pieces of a reduction of K elements: n of len elements (a multiple of 128)
 // whose rows fit a stage; the last may be shorter (its box reads on into what
@@ -395,7 +416,8 @@ struct Pieces {
 };
 __host__ __device__ __forceinline__ Pieces pieces(int K, int esz) {
     Pieces p;
-    p.n = (K * esz + kRowBytes - 1) / kRowBytes;
+    const int row_bytes = kStageAtoms * 128;
+    p.n = (K * esz + row_bytes - 1) / row_bytes;
     p.len = ((K + p.n - 1) / p.n + 127) / 128 * 128;
     p.n = (K + p.len - 1) / p.len;
     return p;
@@ -429,66 +451,54 @@ __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int la
     const Pieces pu = pieces(d, esz), pd = pieces(I, esz);
     const size_t SI = (size_t)S * I;
     const int atoms_u = pu.len * esz / 128, atoms_d = pd.len * esz / 128;
-    auto run_start = [&](int run, int units) {
-        return (int)((long long)run * units / gridDim.x);
-    };
-    // The first run is one of shared gate/up units: its first rows go to L2 now,
-    // while the logits are being made.  (Which CTA takes a run is open, but
-    // together they take these.)
-    if (lane == 0) {
-        const int last = run_start(blockIdx.x + 1, shared_units);
-        int u = run_start(blockIdx.x, shared_units);
-        for (int i = 0; i < kAhead && u < last; ++i, ++u)
-            for (int c = 0; c < pu.n; ++c) box_4d_to_l2(&a.up_map[0], u * 8, c * atoms_u);
-    }
-    pdl_wait();  // the control words are reset
+    const int grid = (int)gridDim.x;
+    auto cut = [&](int run, int units) { return (int)((long long)run * units / grid); };
     int slot = 0, phase = 0;
-    int part = 0, ticket = 0, ahead = 0;
-    int total = shared_units;
-    bool ok = true, took_ahead = false;
-    if (lane == 0) ticket = atomicAdd(a.ctrl + kCtrlTicket, 1);
-    // a stage that carries no weights
-    auto put_word = [&](int what, int tile) {
-        ok = mbar_wait_bounded(s.empty + slot, phase ^ 1, s.abort, a.status, SITE_GEMM_PRODUCER,
-                               a.wait_limit_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        if (lane == 0) {
-            s.info[slot] = make_int4(what, part, tile, 0);
-            mbar_arrive(s.full + slot);
-        }
-        if (FP8) copies_arrive(s.full + slot);
+    int part = 0, run = blockIdx.x;
+    bool ok = true, mine = true;
+    int ahead = 0;        // the claim of this CTA's own run of the next part: 0 if it got it
+    auto next_stage = [&]() {
         if (++slot == a.stages) {
             slot = 0;
             phase ^= 1;
         }
     };
-    while (ok && part < kParts) {
-        ticket = __shfl_sync(0xffffffffu, ticket, 0);
-        if (ticket >= (int)gridDim.x) {  // all runs of this part are taken
-            ticket = ahead;
-            if (!took_ahead && lane == 0 && part + 1 < kParts)
-                ticket = atomicAdd(a.ctrl + kCtrlTicket + 8 * (part + 1), 1);
-            took_ahead = false;
-            ++part;
-            if (part == PART_ROUTED_UP) {
-                ok = mbar_wait_bounded(s.routed, 0, s.abort, a.status, SITE_GEMM_PRODUCER,
-                                       a.wait_limit_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
-            total = part == PART_ROUTED_UP ? (*s.n_entries - S) * up_tiles
-                    : part == PART_DOWN    ? *s.n_entries * down_tiles
-                                           : down_tiles;
-            continue;
+    auto wait_slot = [&]() {
+        const bool free = mbar_wait_bounded(s.empty + slot, phase ^ 1, s.abort, a.status,
+                                            SITE_GEMM_PRODUCER, a.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, free);
+        return ok;
+    };
+    // a stage that carries no weights
+    auto put_word = [&](int what, int tile) {
+        if (!wait_slot()) return;
+        if (lane == 0) {
+            s.info[slot] = make_int4(what, part, tile, 0);
+            mbar_arrive(s.full + slot);
         }
-        const int first = run_start(ticket, total), last = run_start(ticket + 1, total);
-        // the next part's ticket: the answer is there when this run is done (not
-        // so this part's: the CTAs that start first would take two runs each)
-        if (!took_ahead && part + 1 < kParts) {
-            if (lane == 0) ahead = atomicAdd(a.ctrl + kCtrlTicket + 8 * (part + 1), 1);
-            took_ahead = true;
+        if (FP8) copies_arrive(s.full + slot);
+        next_stage();
+    };
+    while (part < kParts) {
+        const int routed_units = part == 0 ? 0 : (*s.n_entries - S) * up_tiles;
+        // units [first, last) of the run: shared and routed gate/up runs of one
+        // number differ by at most one unit together
+        int first, last;
+        if (part == PART_SHARED_UP) {
+            first = cut(run, shared_units);
+            last = cut(run + 1, shared_units);
+        } else if (part == PART_ROUTED_UP && routed_units >= grid) {
+            const int all_units = shared_units + routed_units;
+            first = cut(run, all_units) - cut(run, shared_units);
+            last = cut(run + 1, all_units) - cut(run + 1, shared_units);
+        } else {
+            const int units = part == PART_ROUTED_UP ? routed_units
+                              : part == PART_DOWN    ? *s.n_entries * down_tiles
+                                                     : down_tiles;
+            first = cut(run, units);
+            last = cut(run + 1, units);
         }
+        if (!mine) last = first;
         const bool is_up = part < PART_DOWN;
         const Pieces p = is_up ? pu : pd;
         const int K = is_up ? d : I;
@@ -523,10 +533,7 @@ __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int la
                 }
             }
             for (int c = 0; c < p.n; ++c) {
-                ok = mbar_wait_bounded(s.empty + slot, phase ^ 1, s.abort, a.status,
-                                       SITE_GEMM_PRODUCER, a.wait_limit_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                if (!wait_slot()) break;
                 const int k0 = c * p.len, len = min(p.len, K - k0);
                 if (lane == 0) {
                     s.info[slot] = make_int4(is_up ? WHAT_UP : WHAT_DOWN, entry, tile, c);
@@ -543,15 +550,55 @@ __device__ __forceinline__ void producer(const FewArgs& a, const Smem& s, int la
                         copy_scale(s.scales + slot * 32 + lane, sc + k0 / 128 + (lane & 15));
                     copies_arrive(s.full + slot);
                 }
-                if (++slot == a.stages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                next_stage();
             }
         }
+        if (ok && part != PART_Y && mine) put_word(WHAT_TOLD, 0);
         if (!ok) break;
-        if (part != PART_Y) put_word(WHAT_TOLD, 0);
-        if (lane == 0) ticket = atomicAdd(a.ctrl + kCtrlTicket + 8 * part, 1);
+        // the sum warps have claimed this CTA's first runs by now
+        if (part == 0) {
+            const bool known = mbar_wait_bounded(s.claimed, 0, s.abort, a.status,
+                                                 SITE_GEMM_PRODUCER, a.wait_limit_ns);
+            ok = __all_sync(0xffffffffu, known);
+            if (!ok) break;
+            ahead = *s.ahead;
+        }
+        // a run of this part that no CTA has claimed?
+        mine = false;
+        int claims[kMaxGrid / 32];
+#pragma unroll
+        for (int i = 0; i < kMaxGrid / 32; ++i) {
+            claims[i] = 1;
+            if (32 * i + lane < grid)
+                asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];"
+                             : "=r"(claims[i])
+                             : "l"(a.ctrl + kCtrlClaim + kMaxGrid * part + 32 * i + lane)
+                             : "memory");
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxGrid / 32; ++i) {
+            for (uint32_t vote = __ballot_sync(0xffffffffu, claims[i] == 0); vote != 0 && !mine;
+                 vote &= vote - 1) {
+                run = 32 * i + __ffs(vote) - 1;
+                int got = 0;
+                if (lane == 0)
+                    got = atomicExch(a.ctrl + kCtrlClaim + kMaxGrid * part + run, 1) == 0;
+                mine = __shfl_sync(0xffffffffu, got, 0);
+            }
+        }
+        if (mine) continue;
+        // the next part, from this CTA's own run on
+        ++part;
+        run = blockIdx.x;
+        if (part == PART_ROUTED_UP) {
+            const bool there = mbar_wait_bounded(s.routed, 0, s.abort, a.status,
+                                                 SITE_GEMM_PRODUCER, a.wait_limit_ns);
+            ok = __all_sync(0xffffffffu, there);
+            if (!ok) break;
+        }
+        mine = __shfl_sync(0xffffffffu, ahead, 0) == 0;
+        if (lane == 0 && part + 1 < kParts)
+            ahead = atomicExch(a.ctrl + kCtrlClaim + kMaxGrid * (part + 1) + run, 1);
     }
     if (ok) put_word(WHAT_END, 0);
     if (!ok) {
@@ -652,7 +699,7 @@ __device__ __forceinline__ void fill_b(const Smem& s, const __nv_bfloat16* src, 
 }
 
 // This warp's part of one stage: blocks of 128 whose number (counted over the
-// whole reduction) is the warp's modulo 8.
+// whole reduction) is the warp's modulo the number of warps.
 template <int NT, bool FP8>
 __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, const float* scales,
                                           int k0, int len, bool up, int warp, int lane,
@@ -663,7 +710,7 @@ __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, con
     // this lane's chunk of group 0 and 1 of an atom, swizzled
     const int pos[2] = {((2 * (lane & 3)) ^ row) << 4, ((2 * (lane & 3) + 1) ^ row) << 4};
     const int first = k0 / 128;
-    for (int j = (warp - first) & 7; j < len / 128; j += kWarps) {
+    for (int j = (warp - first) & (kWarps - 1); j < len / 128; j += kWarps) {
         if constexpr (!FP8) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {  // 32 elements each, 2 atoms
@@ -679,11 +726,11 @@ __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, con
                 }
             }
         } else {
-            float part[NT][4];
+            float part[2][NT][4];  // two chains of products
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
+                for (int q = 0; q < 4; ++q) part[0][n][q] = part[1][n][q] = 0.f;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {  // 64 elements each, 1 atom
                 const int at = j * kAtomBytes + pos[g];
@@ -701,18 +748,18 @@ __device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, con
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint4 v = bp[((q >> 1) * NT + n) * 32];
-                        mma16816_f16(part[n], a[0], a[1], a[2], a[3], v.x, v.y);
-                        mma16816_f16(part[n], a[4], a[5], a[6], a[7], v.z, v.w);
+                        mma16816_f16(part[0][n], a[0], a[1], a[2], a[3], v.x, v.y);
+                        mma16816_f16(part[1][n], a[4], a[5], a[6], a[7], v.z, v.w);
                     }
                 }
             }
             const float s0 = scales[j], s1 = up ? scales[16 + j] : s0;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(part[n][0], s0, acc[n][0]);
-                acc[n][1] = fmaf(part[n][1], s0, acc[n][1]);
-                acc[n][2] = fmaf(part[n][2], s1, acc[n][2]);
-                acc[n][3] = fmaf(part[n][3], s1, acc[n][3]);
+                acc[n][0] = fmaf(part[0][n][0] + part[1][n][0], s0, acc[n][0]);
+                acc[n][1] = fmaf(part[0][n][1] + part[1][n][1], s0, acc[n][1]);
+                acc[n][2] = fmaf(part[0][n][2] + part[1][n][2], s1, acc[n][2]);
+                acc[n][3] = fmaf(part[0][n][3] + part[1][n][3], s1, acc[n][3]);
             }
         }
     }
@@ -845,13 +892,23 @@ __device__ __forceinline__ void sums(const FewArgs& a, const Smem& s, int who, i
     // ---- routing: every CTA chooses for itself, CTA 0 writes it out
     const int tid = who * 32 + lane;
     for (int e = tid; e < E; e += 32 * kSumWarps) s.s_mask[e] = 0;
-    pdl_wait();
-    for (int i = tid; i < T * E; i += 32 * kSumWarps)
-        s.keys[i] = __float_as_uint(__ldcg(a.logits + i));
+    pdl_wait();  // the control words are reset, the logits there
+    if (tid == 0) {
+        int* claim = a.ctrl + kCtrlClaim + blockIdx.x;
+        *s.first_mine = atomicExch(claim, 1) == 0;
+        *s.ahead = atomicExch(claim + kMaxGrid, 1);
+        mbar_arrive(s.claimed);
+    }
     sums_sync();
     for (int t = who; t < T; t += kSumWarps) {
-        choose(s.keys + t * E, lane, E, k, a.G, a.TG, a.gate, a.bias, s.s_idx + t * k,
-               s.s_w + t * k);
+        uint32_t* key = s.keys + who * E;
+        int* idx = s.s_idx + t * k;
+        float* w = s.s_w + t * k;
+        const float* lg = a.logits + (size_t)t * E;
+        if (E <= 64)
+            choose<2>(lg, key, lane, E, k, a.G, a.TG, a.gate, a.bias, idx, w);
+        else
+            choose<kMaxE / 32>(lg, key, lane, E, k, a.G, a.TG, a.gate, a.bias, idx, w);
         __syncwarp();
         if (lane < k) {
             atomicOr(s.s_mask + s.s_idx[t * k + lane], 1u << t);
@@ -878,10 +935,19 @@ __device__ __forceinline__ void sums(const FewArgs& a, const Smem& s, int who, i
     sums_sync();
 
     // ---- units
+    bool first_lost = false;
     int told_entry = 0, untold = 0;  // gate/up units stored and not told yet
+    bool checked = false;
     auto tell = [&]() {
         __syncwarp();
-        if (lane == 0 && untold > 0) {
+        if (!checked) {
+            // the first run's units count if the run is this CTA's
+            checked = true;
+            const bool known = mbar_wait_bounded(s.claimed, 0, s.abort, a.status,
+                                                 SITE_GEMM_EPILOGUE, a.wait_limit_ns);
+            if (!known || !*s.first_mine) first_lost = true;
+        }
+        if (lane == 0 && untold > 0 && !first_lost) {
             __threadfence();
             atomicAdd(a.ctrl + kCtrlH + told_entry, untold);
         }
@@ -893,7 +959,7 @@ __device__ __forceinline__ void sums(const FewArgs& a, const Smem& s, int who, i
         if (!__all_sync(0xffffffffu, filled)) return;
         const int4 info = s.unit[who];
         const int buf = unit % kSumBufs;
-        const float4* red = s.red + buf * kWarps * NT * 32 + lane;
+            const float4* red = s.red + buf * kWarps * NT * 32 + lane;
         float4 sum[NT];
         if (info.x == WHAT_UP || info.x == WHAT_DOWN) {
 #pragma unroll
@@ -915,6 +981,7 @@ __device__ __forceinline__ void sums(const FewArgs& a, const Smem& s, int who, i
         if (info.x == WHAT_END) return;
         if (info.x == WHAT_TOLD) {
             tell();
+            first_lost = false;  // the first run is over
             if (info.y == PART_DOWN && lane == 0) {
                 __threadfence();
                 atomicAdd(a.ctrl + kCtrlDown, 1);
@@ -1001,6 +1068,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             mbar_init(s.empty + i, kWarps);
         }
         mbar_init(s.routed, 1);
+        mbar_init(s.claimed, 1);
         mbar_init(s.meet, kWarps);
         for (int i = 0; i < kSumWarps; ++i) mbar_init(s.sum_full + i, kWarps);
         for (int i = 0; i < kSumBufs; ++i) mbar_init(s.sum_empty + i, 1);
@@ -1021,13 +1089,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
 // ---------------------------------------------------------------- host
 enum FewRegion : int { FW_STATUS, FW_CTRL, FW_LOGITS, FW_H, FW_SLOTS, FW_TOTAL };
 
-int few_stages(int T, int d, int E, int I) {
+// stages of the ring (0: operand B leaves too little room for one)
+int few_stages(int T, int d, int I) {
     const int nt = T > 8 ? 2 : 1;
     const long long fixed = (long long)8 * nt * 2 * (d > I ? d : I) +
-                            (nt == 1 ? red_bytes<1>() : red_bytes<2>()) + kSmallBytes +
-                            4 * T * E;
-    const long long n = (kSmemMax - fixed) / kStageBytes;
-    return n < 2 ? 0 : (int)std::min<long long>(n, kMaxStages);
+                            nt * red_bytes<1>() + kSmallBytes;
+    const long long ring = kSmemMax - fixed;
+    if (ring < kMinRing) return 0;
+    return (int)std::min<long long>(ring / kStageBytes, kMaxStages);
 }
 
 int few_check(int T, int d, int E, int k, int inter, int n_shared) {
@@ -1035,7 +1104,7 @@ int few_check(int T, int d, int E, int k, int inter, int n_shared) {
         n_shared < 0)
         return MOE_ERR_INVALID_ARG;
     if (d % 256 != 0 || inter % 128 != 0 || n_shared > kMaxShared || T > kFewMaxT ||
-        (long long)n_shared * inter > INT_MAX / 2 || few_stages(T, d, E, inter) == 0)
+        (long long)n_shared * inter > INT_MAX / 2 || few_stages(T, d, inter) == 0)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -1058,11 +1127,10 @@ bool few_layout(int T, int d, int E, int k, int inter, int n_shared, size_t (&of
 template <int NT, bool FP8>
 cudaError_t launch_layer(const FewArgs& a, cudaStream_t s) {
     auto kern = few_layer_kernel<NT, FP8>;
-    const int smem = a.stages * kStageBytes + b_bytes<NT>(a.d, a.I) + red_bytes<NT>() + kSmallBytes +
-                     4 * a.T * a.E;
+    const int smem = a.stages * kStageBytes + b_bytes<NT>(a.d, a.I) + red_bytes<NT>() + kSmallBytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)num_sms()), dim3(kFewThreads), (size_t)smem, s, 1, a);
+    return launch_pdl(kern, dim3((unsigned)std::min(num_sms(), kMaxGrid)), dim3(kFewThreads), (size_t)smem, s, 1, a);
 }
 
 }  // namespace
@@ -1147,7 +1215,7 @@ MOE_API int moe_forward_few(const void* x, const void* W_router, const void* W_g
     a.I = inter;
     a.S = n_shared;
     a.out_f32 = out_dt == MOE_F32;
-    a.stages = few_stages(T, d, E, inter);
+    a.stages = few_stages(T, d, inter);
     a.y = y;
     a.idx_out = topk_idx_out;
     a.w_out = topk_w_out;
