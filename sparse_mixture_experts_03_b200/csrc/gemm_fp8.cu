@@ -57,7 +57,8 @@ struct Shape8 {
 };
 
 template <int STAGES>
-struct Tail8 {
+struct __align__(16) Tail8 {
+    uint4 out[kEpiWarps8][128];  // per adding warp: 32 rows x 64 bytes on their way out
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
     uint64_t tfull[2];
@@ -159,49 +160,81 @@ __device__ __forceinline__ Tile8 decode8(const TAIL* t, int G, int n_tiles, int 
     return r;
 }
 
-// 32 columns of a row from sums in registers
+// Columns col .. col + 2 W - 1 of the warp's 32 rows (lane = row; `rows` of them
+// exist) from sums in registers.  A lane's 64 bytes at a time go through the
+// warp's staging rows (16-byte chunk q of row r at q ^ (r / 2 % 4): both sides
+// without bank conflicts), so that each store instruction writes 8 whole
+// 64-byte row pieces; straight from the lanes, 16 bytes of 32 rows, the stores
+// of a tile took about 4 us.  Rows of y that are not 16-byte aligned are
+// written from the lanes.
 template <int W>
-__device__ __forceinline__ void store_cols(const Fp8Args& a, size_t row, int col,
-                                           const uint64_t (&acc)[W]) {
-    const size_t base = row * (size_t)a.n + col;
-    if (a.out_f32) {
-        float* y = static_cast<float*>(a.y) + base;
-        if (a.n % 4 == 0) {
+__device__ __forceinline__ void store_rows(const Fp8Args& a, uint4* stage, size_t row0, int rows,
+                                           int col, int lane, const uint64_t (&acc)[W]) {
+    const int per16 = a.out_f32 ? 4 : 8;  // columns in 16 bytes
+    if (a.n % per16 != 0) {
+        if (lane >= rows) return;
+        const size_t base = (row0 + lane) * (size_t)a.n + col;
 #pragma unroll
-            for (int i = 0; i < W; i += 2) {
-                const float2 u = unpair(acc[i]), v = unpair(acc[i + 1]);
-                if (col + 2 * i < a.n)
-                    *reinterpret_cast<float4*>(y + 2 * i) = make_float4(u.x, u.y, v.x, v.y);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float2 u = unpair(acc[i]);
+        for (int i = 0; i < W; ++i) {
+            const float2 u = unpair(acc[i]);
+            if (a.out_f32) {
+                float* y = static_cast<float*>(a.y) + base;
                 if (col + 2 * i < a.n) y[2 * i] = u.x;
                 if (col + 2 * i + 1 < a.n) y[2 * i + 1] = u.y;
+            } else {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + base;
+                if (col + 2 * i < a.n) y[2 * i] = __float2bfloat16_rn(u.x);
+                if (col + 2 * i + 1 < a.n) y[2 * i + 1] = __float2bfloat16_rn(u.y);
             }
         }
         return;
     }
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + base;
-    if (a.n % 8 == 0) {
+    const int sw = (lane >> 1) & 3;
+    const int q = lane & 3;  // chunk of the row pieces this lane stores
+    // 64 bytes: 8 pairs of fp32, 16 pairs of bf16
+    auto flush = [&](int first_col) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 u = unpair(acc[i + q]);
-                w[q] = pack_bf16x2(u.x, u.y);
+        for (int it = 0; it < 4; ++it) {
+            const int r = it * 8 + (lane >> 2);
+            const int c = first_col + q * per16;
+            const uint4 v = stage[r * 4 + (q ^ ((r >> 1) & 3))];
+            if (r < rows && c < a.n) {
+                const size_t at = (row0 + r) * (size_t)a.n + c;
+                if (a.out_f32)
+                    *reinterpret_cast<uint4*>(static_cast<float*>(a.y) + at) = v;
+                else
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + at) = v;
             }
-            if (col + 2 * i < a.n)
-                *reinterpret_cast<uint4*>(y + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+    };
+    if (a.out_f32) {
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = unpair(acc[i + 2 * j]), v = unpair(acc[i + 2 * j + 1]);
+                stage[lane * 4 + (j ^ sw)] =
+                    make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x),
+                               __float_as_uint(v.y));
+            }
+            flush(col + 2 * i);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const float2 u = unpair(acc[i]);
-            if (col + 2 * i < a.n) y[2 * i] = __float2bfloat16_rn(u.x);
-            if (col + 2 * i + 1 < a.n) y[2 * i + 1] = __float2bfloat16_rn(u.y);
+        for (int i = 0; i < W; i += 16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 u = unpair(acc[i + 4 * j + k]);
+                    w[k] = pack_bf16x2(u.x, u.y);
+                }
+                stage[lane * 4 + (j ^ sw)] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            flush(col + 2 * i);
         }
     }
 }
@@ -357,20 +390,30 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
         constexpr int kCols = BN / 2;  // columns of this warp
         const int wq = warp & 3, half = (warp - 4) >> 2;
         const int nb = (a.n + 127) / 128;
+        const int r = wq * 32 + lane;
+        uint4* stage = tail->out[warp - 4];
         int blk = 0;
         bool ok = true;
+        // a tile's scales: of this lane's row and of the columns' block (columns
+        // behind n belong to no block of b: any scale will do)
+        Tile8 t{};
+        const float *sa = nullptr, *sb = nullptr;
+        float sa_next = 0.f, sb_next = 0.f;
+        bool live = false;
+        auto open = [&](int tile) {
+            t = decode8(tail, a.G, n_tiles, tile);
+            live = r < t.rows;
+            sa = a.sa + t.row0 + r;
+            sb = a.sb +
+                 ((size_t)t.g * nb + min((t.nt * BN + half * kCols) / 128, nb - 1)) * kb_n;
+            sa_next = live ? __ldg(sa) : 0.f;
+            sb_next = __ldg(sb);
+        };
+        if ((int)blockIdx.x < total) open(blockIdx.x);
         for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-            const Tile8 t = decode8(tail, a.G, n_tiles, tile);
-            const int r = wq * 32 + lane;
-            const int col0 = t.nt * BN + half * kCols;
-            const bool live = r < t.rows;
-            const float* sa = a.sa + t.row0 + r;
-            // columns behind n belong to no block of b: any scale will do
-            const float* sb = a.sb + ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * kb_n;
             uint64_t acc[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
-            float sa_next = live ? __ldg(sa) : 0.f, sb_next = __ldg(sb);
             for (int kb = 0; kb < kb_n; ++kb, ++blk) {
                 const float sc = sa_next * sb_next;
                 const uint64_t s2 = pair2(sc, sc);
@@ -386,22 +429,29 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
                 tc_fence_after();
                 const uint32_t ta = tmem + (uint32_t)(buf * BN + half * kCols) +
                                     ((uint32_t)(wq * 32) << 16);
+                // the next 32 columns are on their way while these are added
+                uint32_t v[2][32];
+                tmem_ld32(ta, v[0]);
 #pragma unroll
                 for (int c = 0; c < kCols / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(ta + 32 * c, v);
                     tmem_ld_wait();
+                    if (c + 1 < kCols / 32) tmem_ld32(ta + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[16 * c + i] =
-                            fma_pair(pair2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                     s2, acc[16 * c + i]);
+                        acc[16 * c + i] = fma_pair(pair2(__uint_as_float(v[c & 1][2 * i]),
+                                                         __uint_as_float(v[c & 1][2 * i + 1])),
+                                                   s2, acc[16 * c + i]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tail->tempty[buf]);
             }
-            if (ok && live) store_cols(a, (size_t)t.row0 + r, col0, acc);
+            if (!ok) break;
+            // the next tile's scales are on their way while this one is stored
+            const size_t row0 = (size_t)t.row0 + wq * 32;
+            const int rows = t.rows - wq * 32, col0 = t.nt * BN + half * kCols;
+            if (tile + (int)gridDim.x < total) open(tile + gridDim.x);
+            store_rows(a, stage, row0, rows, col0, lane, acc);
         }
     }
     pdl_trigger();
