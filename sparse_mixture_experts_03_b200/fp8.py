@@ -1,0 +1,96 @@
+"""The MoE layer on 8-bit expert weights (e4m3, one scale per 128 x 128 block).
+
+The layer of moe.forward for serving, at half the weight bytes: the router
+stays as it is, the experts' weights are quantised once when the layer is made.
+Up to moe.few_max_tokens() tokens the layer is one call (moe.forward_few, whose
+activations stay 16-bit); above that it is
+
+  1. dispatch   route and copy each chosen (token, expert) row into expert order
+  2. quantise   rows to 8 bits, one scale per 128 columns
+  3. gate/up    8-bit grouped product, bf16 rows
+  4. SwiGLU     and back to 8 bits, each row's gate weight in its scales
+  5. down       8-bit grouped product: the weighted expert rows, bf16
+  6. combine    y[t] = shared experts(x_t) + the token's k rows, in top-k order
+
+with steps 2-5 once more for the shared experts, on all tokens.
+
+Every computing step is a call into the CUDA library; this module only holds
+the weights and passes buffers on.  There is no CPU fallback.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import moe
+
+
+class Fp8MoE:
+    """One layer on 8-bit expert weights.
+
+    W_router [E, d] stays as given; W_gate_up [E, 2 inter, d], W_down [E, d,
+    inter] and W_shared (moe.forward's layouts, bfloat16 or float32) are
+    quantised here and not kept.  x is bfloat16, d a multiple of 256.
+    """
+
+    def __init__(self, W_router, W_gate_up, W_down, W_shared, k: int, n_group: int,
+                 topk_group: int, inter: int, n_shared: int,
+                 out_dtype: torch.dtype = torch.float32, gate: str = "sigmoid",
+                 expert_bias: Optional[torch.Tensor] = None):
+        self.W_router = W_router
+        self.E, self.d = W_router.shape
+        self.k, self.n_group, self.topk_group = k, n_group, topk_group
+        self.inter, self.n_shared = inter, n_shared
+        self.out_dtype, self.gate, self.expert_bias = out_dtype, gate, expert_bias
+        if (n_shared > 0) != (W_shared is not None):
+            raise ValueError("W_shared is given exactly when there are shared experts")
+        self.W_gate_up, self.s_gate_up = moe.quantize_weight(W_gate_up)
+        self.W_down, self.s_down = moe.quantize_weight(W_down)
+        self.W_shared = self.s_shared = None
+        if n_shared:
+            SI, d = n_shared * inter, self.d
+            n_gu = 2 * SI * d
+            self.W_shared = torch.empty(W_shared.numel(), dtype=moe.E4M3, device=W_shared.device)
+            self.s_shared = torch.empty(W_shared.numel() // (128 * 128), dtype=torch.float32,
+                                        device=W_shared.device)
+            n_s = n_gu // (128 * 128)
+            self.shared_gate_up = (self.W_shared[:n_gu].view(2 * SI, d),
+                                   self.s_shared[:n_s].view(2 * SI // 128, d // 128))
+            self.shared_down = (self.W_shared[n_gu:].view(d, SI),
+                                self.s_shared[n_s:].view(d // 128, SI // 128))
+            moe.quantize_weight(W_shared[:n_gu].view(2 * SI, d), *self.shared_gate_up)
+            moe.quantize_weight(W_shared[n_gu:].view(d, SI), *self.shared_down)
+        self.few = moe.few_max_tokens(self.d, self.E, k, inter, n_shared)
+
+    def shared(self, x: torch.Tensor) -> Optional[torch.Tensor]:
+        """The shared experts' sum, fp32 [T, d] (None without shared experts)."""
+        if not self.n_shared:
+            return None
+        gate_up = moe.matmul_fp8(*moe.quantize_rows(x), *self.shared_gate_up)
+        return moe.matmul_fp8(*moe.swiglu_quantize_rows(gate_up), *self.shared_down,
+                              out_dtype=torch.float32)
+
+    def experts(self, rows: torch.Tensor, w: torch.Tensor, counts: torch.Tensor) -> torch.Tensor:
+        """w[r] * expert of row r, bfloat16; rows in expert order, counts[e] of
+        expert e."""
+        gate_up = moe.matmul_fp8(*moe.quantize_rows(rows), self.W_gate_up, self.s_gate_up, counts)
+        return moe.matmul_fp8(*moe.swiglu_quantize_rows(gate_up, w), self.W_down, self.s_down,
+                              counts)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        T = x.shape[0]
+        if T <= self.few:
+            return moe.forward_few(x, self.W_router, self.W_gate_up, self.W_down, self.W_shared,
+                                   self.k, self.n_group, self.topk_group, self.inter,
+                                   self.n_shared, scales=(self.s_gate_up, self.s_down,
+                                                          self.s_shared),
+                                   out_dtype=self.out_dtype, gate=self.gate,
+                                   expert_bias=self.expert_bias)
+        disp = moe.dispatch(x, self.W_router, self.k, self.n_group, self.topk_group,
+                            gate=self.gate, expert_bias=self.expert_bias)
+        y_shared = self.shared(x)
+        rows = self.experts(disp.x_perm, disp.w_perm, disp.counts)
+        return moe.combine(rows, disp.slot_row, y_shared, T, self.k, self.out_dtype)
+
+    __call__ = forward

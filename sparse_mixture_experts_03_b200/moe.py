@@ -464,24 +464,35 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, shared: Optional[torch.T
 E4M3 = torch.float8_e4m3fn
 
 
-def _want(name: str, t: torch.Tensor, shape, dtype, like: torch.Tensor) -> None:
-    """The tensor that an entry point expects: the library sees only its
-    pointer, so its shape, type and device are checked here."""
+# The calls below take a few microseconds on the GPU at decode sizes, so their
+# host side is kept short: pointers go to ctypes as plain numbers, and the
+# current stream is asked for as its handle.
+
+def _want(name: str, t: torch.Tensor, shape, dtype, like: torch.Tensor) -> int:
+    """The address of a tensor that an entry point expects: the library sees
+    only that, so its shape, type, layout and device are checked here."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _on_current(name: str, t: torch.Tensor) -> None:
-    """The library works on the current CUDA device."""
-    if t.device.type != "cuda":
+def _on_current(name: str, t: torch.Tensor, stream) -> Tuple[int, int]:
+    """(address, stream handle): the library works on the current CUDA device."""
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr(), (torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                          else stream.cuda_stream)
 
 
 def _blocks(n: int) -> int:
@@ -496,18 +507,22 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     dt = _dt(x)
     if x.dim() != 2:
         raise ValueError(f"x must be [R, d], got {tuple(x.shape)}")
-    _on_current("x", x)
+    px, s = _on_current("x", x, stream)
     R, d = x.shape
     if q is None:
-        q = torch.empty(R, d, dtype=E4M3, device=x.device)
+        q = torch.empty((R, d), dtype=E4M3, device=x.device)
+        pq = q.data_ptr()
     else:
-        _want("q", q, (R, d), E4M3, x)
+        pq = _want("q", q, (R, d), E4M3, x)
+    shape = (_blocks(d), R)
     if scales is None:
-        scales = torch.empty(_blocks(d), R, dtype=torch.float32, device=x.device)
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        ps = scales.data_ptr()
     else:
-        _want("scales", scales, (_blocks(d), R), torch.float32, x)
-    _check(lib().moe_quantize_rows(_ptr(x), R, d, dt, _ptr(q), _ptr(scales), _stream(stream)),
-           "moe_quantize_rows")
+        ps = _want("scales", scales, shape, torch.float32, x)
+    st = lib().moe_quantize_rows(px, R, d, dt, pq, ps, s)
+    if st:
+        _check(st, "moe_quantize_rows")
     return q, scales
 
 
@@ -521,21 +536,23 @@ def swiglu_quantize_rows(gate_up: torch.Tensor, w: Optional[torch.Tensor] = None
     dt = _dt(gate_up)
     if gate_up.dim() != 2 or gate_up.shape[1] % 2:
         raise ValueError(f"gate_up must be [R, 2*inter], got {tuple(gate_up.shape)}")
-    _on_current("gate_up", gate_up)
+    px, s = _on_current("gate_up", gate_up, stream)
     R, inter = gate_up.shape[0], gate_up.shape[1] // 2
-    if w is not None:
-        _want("w", w, (R,), torch.float32, gate_up)
+    pw = None if w is None else _want("w", w, (R,), torch.float32, gate_up)
     if q is None:
-        q = torch.empty(R, inter, dtype=E4M3, device=gate_up.device)
+        q = torch.empty((R, inter), dtype=E4M3, device=gate_up.device)
+        pq = q.data_ptr()
     else:
-        _want("q", q, (R, inter), E4M3, gate_up)
+        pq = _want("q", q, (R, inter), E4M3, gate_up)
+    shape = (_blocks(inter), R)
     if scales is None:
-        scales = torch.empty(_blocks(inter), R, dtype=torch.float32, device=gate_up.device)
+        scales = torch.empty(shape, dtype=torch.float32, device=gate_up.device)
+        ps = scales.data_ptr()
     else:
-        _want("scales", scales, (_blocks(inter), R), torch.float32, gate_up)
-    _check(lib().moe_swiglu_quantize_rows(_ptr(gate_up), _ptr(w), R, inter, dt, _ptr(q),
-                                          _ptr(scales), _stream(stream)),
-           "moe_swiglu_quantize_rows")
+        ps = _want("scales", scales, shape, torch.float32, gate_up)
+    st = lib().moe_swiglu_quantize_rows(px, pw, R, inter, dt, pq, ps, s)
+    if st:
+        _check(st, "moe_swiglu_quantize_rows")
     return q, scales
 
 
@@ -547,21 +564,23 @@ def quantize_weight(W: torch.Tensor, q: Optional[torch.Tensor] = None,
     dt = _dt(W)
     if W.dim() not in (2, 3):
         raise ValueError(f"W must be [n, k] or [G, n, k], got {tuple(W.shape)}")
-    _on_current("W", W)
+    px, s = _on_current("W", W, stream)
     n, k = W.shape[-2:]
     G = W.shape[0] if W.dim() == 3 else 1
-    lead = tuple(W.shape[:-2])
     if q is None:
         q = torch.empty(W.shape, dtype=E4M3, device=W.device)
+        pq = q.data_ptr()
     else:
-        _want("q", q, W.shape, E4M3, W)
-    shape = lead + (_blocks(n), _blocks(k))
+        pq = _want("q", q, W.shape, E4M3, W)
+    shape = tuple(W.shape[:-2]) + (_blocks(n), _blocks(k))
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=W.device)
+        ps = scales.data_ptr()
     else:
-        _want("scales", scales, shape, torch.float32, W)
-    _check(lib().moe_quantize_weight(_ptr(W), G, n, k, dt, _ptr(q), _ptr(scales),
-                                     _stream(stream)), "moe_quantize_weight")
+        ps = _want("scales", scales, shape, torch.float32, W)
+    st = lib().moe_quantize_weight(px, G, n, k, dt, pq, ps, s)
+    if st:
+        _check(st, "moe_quantize_weight")
     return q, scales
 
 
@@ -575,24 +594,36 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     if a.dim() != 2 or b.dim() not in (2, 3):
         raise ValueError(f"a must be [R, k] and b [n, k] or [G, n, k], got {tuple(a.shape)} "
                          f"and {tuple(b.shape)}")
-    _on_current("a", a)
+    if a.dtype != E4M3:
+        raise TypeError(f"a must be {E4M3}, got {a.dtype}")
+    pa, s = _on_current("a", a, stream)
     R, k = a.shape
+    lead = tuple(b.shape[:-2])
     n = b.shape[-2]
-    G = b.shape[0] if b.dim() == 3 else 1
-    _want("a", a, (R, k), E4M3, a)
-    _want("a_scales", a_scales, (_blocks(k), R), torch.float32, a)
-    _want("b", b, tuple(b.shape[:-1]) + (k,), E4M3, a)
-    _want("b_scales", b_scales, tuple(b.shape[:-2]) + (_blocks(n), _blocks(k)), torch.float32, a)
-    if counts is not None:
-        _want("counts", counts, (G,), torch.int32, a)
+    G = lead[0] if lead else 1
+    psa = _want("a_scales", a_scales, (_blocks(k), R), torch.float32, a)
+    pb = _want("b", b, lead + (n, k), E4M3, a)
+    psb = _want("b_scales", b_scales, lead + (_blocks(n), _blocks(k)), torch.float32, a)
+    pc = None if counts is None else _want("counts", counts, (G,), torch.int32, a)
     if y is None:
-        y = torch.empty(R, n, dtype=out_dtype, device=a.device)
+        y = torch.empty((R, n), dtype=out_dtype, device=a.device)
+        py = y.data_ptr()
     else:
-        _want("y", y, (R, n), y.dtype, a)
-    _check(lib().moe_matmul_fp8(_ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), _ptr(counts),
-                                R, G, n, k, _dt(y), _ptr(y), _ptr(status_ws), _stream(stream)),
-           "moe_matmul_fp8")
+        py = _want("y", y, (R, n), y.dtype, a)
+    st = lib().moe_matmul_fp8(pa, psa, pb, psb, pc, R, G, n, k, _dt(y), py, _status_words(status_ws, a),
+                              s)
+    if st:
+        _check(st, "moe_matmul_fp8")
     return y
+
+
+def _status_words(ws: Optional[torch.Tensor], like: torch.Tensor) -> Optional[int]:
+    """The address of a buffer whose first 256 bytes are status words."""
+    if ws is None:
+        return None
+    if ws.numel() * ws.element_size() < 256:
+        raise ValueError("status_ws must hold 256 bytes")
+    return _want("status_ws", ws, ws.shape, ws.dtype, like)
 
 
 # ---- the layer for a few tokens
@@ -619,42 +650,38 @@ def forward_few(x: torch.Tensor, W_router: torch.Tensor, W_gate_up: torch.Tensor
     """moe_forward_few: forward() for up to few_max_tokens() tokens.  scales:
     None for bfloat16 expert weights, or (s_gate_up, s_down, s_shared or None)
     for e4m3 weights in the same layouts (quantize_weight)."""
-    _on_current("x", x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, d], got {tuple(x.shape)}")
+    px, s = _on_current("x", x, stream)
     T, d = x.shape
     E = W_router.shape[0]
-    wt = torch.bfloat16 if scales is None else E4M3
+    f32, wt = torch.float32, torch.bfloat16 if scales is None else E4M3
     sh = 3 * n_shared * inter * d
-    _want("W_router", W_router, (E, d), x.dtype, x)
-    _want("W_gate_up", W_gate_up, (E, 2 * inter, d), wt, x)
-    _want("W_down", W_down, (E, d, inter), wt, x)
-    if W_shared is not None:
-        _want("W_shared", W_shared, (sh,), wt, x)
+    pr = _want("W_router", W_router, (E, d), x.dtype, x)
+    pg = _want("W_gate_up", W_gate_up, (E, 2 * inter, d), wt, x)
+    pd = _want("W_down", W_down, (E, d, inter), wt, x)
+    psh = None if W_shared is None else _want("W_shared", W_shared, (sh,), wt, x)
     s_gu = s_dn = s_sh = None
     if scales is not None:
-        s_gu, s_dn, s_sh = scales
-        _want("s_gate_up", s_gu, (E, 2 * inter // 128, d // 128), torch.float32, x)
-        _want("s_down", s_dn, (E, d // 128, inter // 128), torch.float32, x)
-        if s_sh is not None:
-            _want("s_shared", s_sh, (sh // (128 * 128),), torch.float32, x)
+        s_gu = _want("s_gate_up", scales[0], (E, 2 * inter // 128, d // 128), f32, x)
+        s_dn = _want("s_down", scales[1], (E, d // 128, inter // 128), f32, x)
+        if scales[2] is not None:
+            s_sh = _want("s_shared", scales[2], (sh // (128 * 128),), f32, x)
     if y is None:
-        y = torch.empty(T, d, dtype=out_dtype, device=x.device)
-    else:
-        _want("y", y, (T, d), y.dtype, x)
-    if topk_idx is not None:
-        _want("topk_idx", topk_idx, (T, k), torch.int32, x)
-    if topk_w is not None:
-        _want("topk_w", topk_w, (T, k), torch.float32, x)
-    if expert_bias is not None:
-        _want("expert_bias", expert_bias, (E,), torch.float32, x)
+        y = torch.empty((T, d), dtype=out_dtype, device=x.device)
+    py = _want("y", y, (T, d), y.dtype, x)
+    pi = None if topk_idx is None else _want("topk_idx", topk_idx, (T, k), torch.int32, x)
+    pw = None if topk_w is None else _want("topk_w", topk_w, (T, k), f32, x)
+    pe = None if expert_bias is None else _want("expert_bias", expert_bias, (E,), f32, x)
     if workspace is None:
         workspace = torch.empty(few_workspace_bytes(T, d, E, k, inter, n_shared),
                                 dtype=torch.uint8, device=x.device)
-    _check(lib().moe_forward_few(_ptr(x), _ptr(W_router), _ptr(W_gate_up), _ptr(W_down),
-                                 _ptr(W_shared), _ptr(s_gu), _ptr(s_dn), _ptr(s_sh), T, d, E, k,
-                                 n_group, topk_group, inter, n_shared, _dt(x), _dt(y),
-                                 GATES[gate], _ptr(expert_bias), _ptr(y), _ptr(topk_idx),
-                                 _ptr(topk_w), _ptr(workspace), workspace.numel(),
-                                 _stream(stream)), "moe_forward_few")
+    pws = _want("workspace", workspace, workspace.shape, torch.uint8, x)
+    st = lib().moe_forward_few(px, pr, pg, pd, psh, s_gu, s_dn, s_sh, T, d, E, k, n_group,
+                               topk_group, inter, n_shared, _dt(x), _dt(y), GATES[gate], pe, py,
+                               pi, pw, pws, workspace.numel(), s)
+    if st:
+        _check(st, "moe_forward_few")
     return y
 
 

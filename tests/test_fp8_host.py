@@ -101,7 +101,7 @@ def test_tensors_are_checked_before_their_pointers():
     q = torch.zeros(4, 256, dtype=moe.E4M3)
     with pytest.raises(ValueError, match="CUDA tensor"):
         moe.matmul_fp8(q, q, q, q)
-    want = moe._want
+    want = moe._want  # noqa: SLF001
     with pytest.raises(ValueError):
         want("t", bf, (4, 255), torch.bfloat16, bf)
     with pytest.raises(TypeError):

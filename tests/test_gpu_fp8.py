@@ -275,3 +275,72 @@ def test_product_on_a_side_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(y2, want)
     del g
+
+
+# ---------------------------------------------------------------- the layer on 8-bit weights
+
+def fp8_layer(E=16, k=4, G=4, TG=2, d=512, I=256, S=2, seed=0, **kw):
+    from sparse_mixture_experts_03_b200.fp8 import Fp8MoE
+    Wr = randn(E, d, seed=seed).mul_(d ** -0.5)
+    gu = randn(E, 2 * I, d, seed=seed + 1).mul_(d ** -0.5)
+    dn = randn(E, d, I, seed=seed + 2).mul_(I ** -0.5)
+    sh = None
+    if S:
+        sh = torch.cat([randn(2 * S * I * d, seed=seed + 3).mul_(d ** -0.5),
+                        randn(S * I * d, seed=seed + 4).mul_(I ** -0.5)])
+    return Fp8MoE(Wr, gu, dn, sh, k, G, TG, I, S, **kw)
+
+
+def layer64(layer, x, idx, w):
+    """The layer in fp64 on its 8-bit weights, for a given routing."""
+    wide = lambda q, s: q.double() * s.double().repeat_interleave(128, -2).repeat_interleave(128, -1)
+    I, SI = layer.inter, layer.n_shared * layer.inter
+    ffn = lambda gu, dn, F, v: (torch.nn.functional.silu(v @ gu[:F].t()) * (v @ gu[F:].t())) @ dn.t()
+    X = x.double()
+    y = torch.zeros_like(X)
+    if SI:
+        y += ffn(wide(*layer.shared_gate_up), wide(*layer.shared_down), SI, X)
+    gu, dn = wide(layer.W_gate_up, layer.s_gate_up), wide(layer.W_down, layer.s_down)
+    for e in range(layer.E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        if t.numel():
+            y[t] += w[t, j, None].double() * ffn(gu[e], dn[e], I, X[t])
+    return y
+
+
+@pytest.mark.parametrize("T,S,out", [(1, 2, torch.float32), (16, 2, torch.bfloat16),
+                                     (17, 2, torch.float32), (300, 2, torch.bfloat16),
+                                     (1100, 0, torch.float32), (33, 1, torch.float32)])
+def test_layer_on_8bit_weights(T, S, out):
+    layer = fp8_layer(S=S, out_dtype=out, seed=T)
+    x = randn(T, 512, seed=T + 9)
+    y = layer(x)
+    idx, w = moe.route(x, layer.W_router, layer.k, layer.n_group, layer.topk_group)
+    ref = layer64(layer, x, idx.long(), w)
+    assert y.dtype == out and y.shape == (T, 512)
+    # Up to 16 tokens only h and y are rounded, to bf16.  Above, rows are rounded
+    # to e4m3: an error spread evenly over half a step either way is at most r =
+    # 2^-4 / sqrt(3) of the norm; x's reaches h through gate (|silu'| <= 1.1) and
+    # up, 2.1 r, and h has its own, r.
+    tol = 5e-3 if T <= layer.few else 3.1 * 2.0 ** -4 / 3 ** 0.5
+    assert float((y.double() - ref).norm() / ref.norm()) <= tol
+    assert torch.equal(y, layer(x))
+
+
+def test_layer_of_no_tokens_and_in_a_graph():
+    layer = fp8_layer(seed=3)
+    assert layer(randn(0, 512)).shape == (0, 512)
+    for T in (5, 40):
+        x = randn(T, 512, seed=T)
+        g = torch.cuda.CUDAGraph()
+        layer(x)  # the libraries' first calls are not captured
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            y = layer(x)
+        for seed in (1, 2):
+            x.copy_(randn(T, 512, seed=seed))
+            g.replay()
+            want = layer(x)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+        del g
