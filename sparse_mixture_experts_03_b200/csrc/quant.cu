@@ -39,7 +39,7 @@ struct BlockScale {
     float scale;  // A / 448 (NaN for a block with an infinity or a NaN)
     float mul;    // 448, or 448 * 2^-20 where 448 A would overflow
     float den;    // A times the same power of two
-    float rcp;    // 1 / den
+    float rcp;    // 1 / den, to an ulp or two
 };
 
 // amax_bits: the bits of max |x| as an fp32 value; infinities and NaN are at
@@ -52,10 +52,13 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
     }
     const float A = fmaxf(__uint_as_float(amax_bits), kAmaxFloor);
     const float pre = A > 1.2676506e30f ? 9.5367431640625e-07f : 1.f;  // above 2^100: 2^-20
-    b.scale = A / kE4m3Max;
+    // A / 448, rounded once: a product with 1 / 448 and its correction (all
+    // lanes of a block do this: a division would be a tenth of the kernel)
+    const float t = A * (1.f / kE4m3Max);
+    b.scale = fmaf(fmaf(-t, kE4m3Max, A), 1.f / kE4m3Max, t);
     b.mul = kE4m3Max * pre;
     b.den = A * pre;
-    b.rcp = 1.f / b.den;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.rcp) : "f"(b.den));  // 2^-108 <= 1 / den <= 2^100
     return b;
 }
 
@@ -87,6 +90,13 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
+__device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+    return m;
+}
+
 // Eight consecutive values of a row, as one lane holds them.
 struct Bf16x8 {
     uint4 v;
@@ -94,6 +104,12 @@ struct Bf16x8 {
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const void* p, size_t i) {
         v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+    }
+    // the bits of the largest magnitude, as fp32
+    __device__ __forceinline__ uint32_t amax() const {
+        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                    __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        return max(m & 0xffff0000u, m << 16);
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -113,6 +129,11 @@ struct F32x8 {
         v[0] = __ldcs(q);
         v[1] = __ldcs(q + 1);
     }
+    __device__ __forceinline__ uint32_t amax() const {
+        float f[8];
+        get(f);
+        return amax_bits8(f);
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -124,13 +145,6 @@ struct F32x8 {
     }
 };
 
-__device__ __forceinline__ uint32_t amax_bits8(const float (&f)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-    return m;
-}
-
 template <bool EXACT>
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], const BlockScale& b) {
     float t[8];
@@ -139,16 +153,11 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], const BlockScale& b
     return make_uint2(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]));
 }
 
-__device__ __forceinline__ uint32_t max_over_16(uint32_t m) {
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-    return m;
-}
-
 // Rows.  CTA: 8 rows; its 8 warps take the rows' 256-column chunks in order, 16
 // lanes per block of 128, 8 columns per lane, kUnroll chunks in flight each.
 // The scales [block][row] leave through shared memory, 32 bytes (8 rows) at a
-// time.  SRC::fetch(i) starts the loads of chunk i, SRC::values gives fp32.
+// time.  SRC::fetch starts a chunk's loads, loaded makes its values, amax and
+// get give them.
 template <typename V>
 struct PlainSrc {
     static constexpr bool kExact = V::kExact;
@@ -157,11 +166,14 @@ struct PlainSrc {
         v.zero();
         if (ok) v.load(x, row * (size_t)d + col);
     }
-    __device__ __forceinline__ void values(float (&f)[8]) const { v.get(f); }
+    __device__ __forceinline__ void loaded() {}
+    __device__ __forceinline__ uint32_t amax() const { return v.amax(); }
+    __device__ __forceinline__ void get(float (&f)[8]) const { v.get(f); }
 };
 struct SwigluSrc {
     static constexpr bool kExact = false;  // h itself is an fp32 result
     Bf16x8 g, u;
+    float h[8];
     __device__ __forceinline__ void fetch(const void* x, size_t row, int d, int col, bool ok) {
         g.zero();
         u.zero();
@@ -172,12 +184,17 @@ struct SwigluSrc {
     }
     // silu(g) u with the hardware exponential: its relative error grows with
     // -g, where silu is small against the block's largest value
-    __device__ __forceinline__ void values(float (&f)[8]) const {
+    __device__ __forceinline__ void loaded() {
         float a[8], b[8];
         g.get(a);
         u.get(b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __fdividef(a[i], 1.f + __expf(-a[i])) * b[i];
+        for (int i = 0; i < 8; ++i) h[i] = __fdividef(a[i], 1.f + __expf(-a[i])) * b[i];
+    }
+    __device__ __forceinline__ uint32_t amax() const { return amax_bits8(h); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = h[i];
     }
 };
 
@@ -190,30 +207,48 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
     const int r0 = blockIdx.x * kQuantRows;
     const int rows = min(kQuantRows, R - r0);
     const int chunks = (d + 255) / 256;
-    const int tasks = rows * chunks;
     pdl_wait();
-    for (int base = warp; base < tasks; base += 8 * UNROLL) {
+    // the next chunk of this warp, 8 further on each time (no division per chunk)
+    const int step_row = 8 / chunks, step_ch = 8 - step_row * chunks;
+    int row_n = warp / chunks, ch_n = warp - row_n * chunks;
+    while (row_n < rows) {
         SRC src[UNROLL];
+        int rows_i[UNROLL], cols_i[UNROLL];
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i) {
-            const int task = base + 8 * i;
-            const int row = task / chunks, col = (task - row * chunks) * 256 + lane * 8;
-            src[i].fetch(x, (size_t)(r0 + row), d, col, task < tasks && col < d);
+            rows_i[i] = row_n;
+            cols_i[i] = row_n < rows ? ch_n * 256 + lane * 8 : d;  // d: nothing there
+            row_n += step_row;
+            ch_n += step_ch;
+            if (ch_n >= chunks) {
+                ch_n -= chunks;
+                ++row_n;
+            }
+            src[i].fetch(x, (size_t)(r0 + rows_i[i]), d, cols_i[i], cols_i[i] < d);
+        }
+        // the blocks' maxima side by side: 16 lanes each
+        uint32_t m[UNROLL];
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            src[i].loaded();
+            m[i] = src[i].amax();
         }
 #pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i)
+                m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+#pragma unroll
         for (int i = 0; i < UNROLL; ++i) {
-            const int task = base + 8 * i;
-            if (task >= tasks) break;  // warp-uniform
-            const int row = task / chunks, ch = task - row * chunks;
-            const int col = ch * 256 + lane * 8;
+            const int row = rows_i[i], col = cols_i[i];
             float f[8];
-            src[i].values(f);
-            const BlockScale b = block_scale(max_over_16(amax_bits8(f)));
+            src[i].get(f);
+            const BlockScale b = block_scale(m[i]);
             if (col < d) {
                 *reinterpret_cast<uint2*>(q + (size_t)(r0 + row) * d + col) =
                     codes8<SRC::kExact>(f, b);
                 if ((lane & 15) == 0)
-                    s_scale[(2 * ch + (lane >> 4)) * kQuantRows + row] =
+                    s_scale[(col >> 7) * kQuantRows + row] =
                         w != nullptr ? b.scale * w[r0 + row] : b.scale;
             }
         }
@@ -248,11 +283,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weight_kernel(
     }
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float f[8];
-        v[i].get(f);
-        m = max(m, amax_bits8(f));
-    }
+    for (int i = 0; i < 8; ++i) m = max(m, v[i].amax());
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) s_max[warp] = m;
     __syncthreads();
@@ -281,7 +312,7 @@ cudaError_t launch_rows(const void* x, const float* w, int R, int d, void* q, fl
                         cudaStream_t s) {
     const int nb = (d + 127) / 128;
     return launch_pdl(quantize_rows_kernel<SRC, UNROLL>,
-                      dim3((unsigned)((R + kQuantRows - 1) / kQuantRows)), dim3(kQuantThreads),
+                      dim3((unsigned)(((long long)R + kQuantRows - 1) / kQuantRows)), dim3(kQuantThreads),
                       sizeof(float) * kQuantRows * nb, s, 1, x, w, R, d, nb,
                       static_cast<uint8_t*>(q), scales);
 }
