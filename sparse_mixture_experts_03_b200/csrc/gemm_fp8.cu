@@ -13,10 +13,11 @@
 //
 // CTA (one per SM, persistent): 128 rows x BN columns.  Warp 0 loads the
 // operands by TMA (128-byte swizzle) into a ring of stages, warp 1 issues the
-// products, warps 4..11 add (two warps per SM sub-partition: TMEM lanes
+// products, warp 2 decodes tiles ahead of them (a search and two divisions, 1 us
+// per tile in the adding warps), warps 4..11 add (two warps per SM sub-partition: TMEM lanes
 // 32 (w % 4).., columns half (w - 4) / 4).  128 sums a thread need more
 // registers than an even split leaves: warps 0..3 hand theirs over (of the
-// launch's 384 x 168, 128 x 56 + 256 x 224).
+// launch's 384 x 168, 128 x 120 + 256 x 192).
 #include <cudaTypedefs.h>
 #include <limits.h>
 
@@ -34,6 +35,7 @@ constexpr int kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (4 + kEpiWarps8);
 constexpr int kABytes8 = kM8 * kK8;
 constexpr uint64_t kDrainNs8 = 1000000;
+constexpr int kTileRing = 4;
 
 struct Fp8Args {
     const float* sa;        // [kb][R]
@@ -41,12 +43,17 @@ struct Fp8Args {
     const int32_t* counts;  // nullptr: one group of R rows
     int R, G, n, k;
     int out_f32;
+    int wide_rows;  // rows of y are 32-byte aligned
     void* y;
     int* status;
     unsigned long long wait_limit_ns;
 };
+// Rows of a are loaded in boxes of 32, 64 or 128: a tile of a few rows (an
+// expert's at decode) does not bring its neighbours' rows along.  What the stage
+// holds behind them is multiplied too, into sums that nobody reads.
+constexpr int kRowBoxes = 3;
 struct Fp8Maps {
-    CUtensorMap a, b;
+    CUtensorMap a[kRowBoxes], b;
 };
 
 template <int BN>
@@ -64,6 +71,9 @@ struct __align__(16) Tail8 {
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
+    uint64_t tile_full[kTileRing];   // a decoded tile is there
+    uint64_t tile_empty[kTileRing];  // the loading lane and the adding warps have it
+    int4 tile[kTileRing];
     uint32_t tmem_base;
     int abort;
     int row_off[kMaxE + 1];   // first row of each group
@@ -138,6 +148,18 @@ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
 struct Tile8 {
     int g, row0, rows, nt;
 };
+// The nth tile of this CTA, as warp 2 decoded it.
+template <class TAIL>
+__device__ __forceinline__ bool take_tile(TAIL* tail, int nth, Tile8& t, volatile int* abort,
+                                          int* status, int site, uint64_t limit) {
+    const int slot = nth % kTileRing;
+    if (!mbar_wait_bounded(&tail->tile_full[slot], (nth / kTileRing) & 1, abort, status, site,
+                           limit))
+        return false;
+    const int4 v = tail->tile[slot];
+    t = Tile8{v.x, v.y, v.z, v.w};
+    return true;
+}
 template <class TAIL>
 __device__ __forceinline__ Tile8 decode8(const TAIL* t, int G, int n_tiles, int tile) {
     // row tiles of a group are neighbours: a weight tile is read from memory once
@@ -186,6 +208,26 @@ __device__ __forceinline__ void store_rows(const Fp8Args& a, uint4* stage, size_
                 if (col + 2 * i < a.n) y[2 * i] = __float2bfloat16_rn(u.x);
                 if (col + 2 * i + 1 < a.n) y[2 * i + 1] = __float2bfloat16_rn(u.y);
             }
+        }
+        return;
+    }
+    if (!a.out_f32 && a.wide_rows) {
+        // 32 bytes per lane and instruction: whole sectors
+        if (lane >= rows) return;
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + (row0 + lane) * (size_t)a.n + col;
+#pragma unroll
+        for (int i = 0; i < W; i += 8) {
+            if (col + 2 * i >= a.n) return;
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 u = unpair(acc[i + k]);
+                w[k] = pack_bf16x2(u.x, u.y);
+            }
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + 2 * i),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                         "r"(w[6]), "r"(w[7])
+                         : "memory");
         }
         return;
     }
@@ -263,6 +305,10 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             mbar_init(&tail->tempty[i], kEpiWarps8);
         }
         mbar_init(&tail->drain, 1);
+        for (int i = 0; i < kTileRing; ++i) {
+            mbar_init(&tail->tile_full[i], 1);
+            mbar_init(&tail->tile_empty[i], 1 + kEpiWarps8);
+        }
         tail->abort = 0;
         fence_barrier_init();
     }
@@ -320,22 +366,28 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
     const int kb_n = (a.k + kK8 - 1) / kK8;
 
     if (warp < 4) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
       if (warp == 0) {
         // ------------------------------------------------ loads
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0, issued = 0, issued_ph = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                const Tile8 t = decode8(tail, a.G, n_tiles, tile);
+            int nth = 0;
+            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++nth) {
+                Tile8 t;
+                ok = take_tile(tail, nth, t, abort_flag, status, SITE_GEMM_PRODUCER, limit);
+                if (!ok) break;
+                mbar_arrive(&tail->tile_empty[nth % kTileRing]);
+                const int box = t.rows <= 32 ? 0 : t.rows <= 64 ? 1 : 2;
+                const uint32_t bytes = (uint32_t)((32 << box) * kK8 + BN * kK8);
                 for (int kb = 0; kb < kb_n; ++kb) {
                     ok = mbar_wait_bounded(&tail->empty[s], ph ^ 1u, abort_flag, status,
                                            SITE_GEMM_PRODUCER, limit);
                     if (!ok) break;
                     uint8_t* st = smem + (size_t)s * SH::kStageBytes;
-                    mbar_arrive_expect_tx(&tail->full[s], SH::kStageBytes);
-                    tma_load_2d(st, &maps.a, &tail->full[s], kb * kK8, t.row0);
+                    mbar_arrive_expect_tx(&tail->full[s], bytes);
+                    tma_load_2d(st, &maps.a[box], &tail->full[s], kb * kK8, t.row0);
                     tma_load_3d(st + kABytes8, &maps.b, &tail->full[s], kb * kK8, t.nt * BN, t.g);
                     issued |= 1u << s;
                     issued_ph = (issued_ph & ~(1u << s)) | (ph << s);
@@ -383,10 +435,24 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             commit8(&tail->drain);
             mbar_wait_bounded(&tail->drain, 0u, nullptr, status, SITE_GEMM_DRAIN, limit);
         }
+      } else if (warp == 2) {
+        // ------------------------------------------------ tiles, decoded
+        if (lane == 0) {
+            int nth = 0;
+            for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
+                const Tile8 t = decode8(tail, a.G, n_tiles, tile);
+                const int slot = nth % kTileRing;
+                if (!mbar_wait_bounded(&tail->tile_empty[slot], ((nth / kTileRing) & 1) ^ 1u,
+                                       abort_flag, status, SITE_GEMM_PRODUCER, limit))
+                    break;
+                tail->tile[slot] = make_int4(t.g, t.row0, t.rows, t.nt);
+                mbar_arrive(&tail->tile_full[slot]);
+            }
+        }
       }
     } else {
         // ------------------------------------------------ sums
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         constexpr int kCols = BN / 2;  // columns of this warp
         const int wq = warp & 3, half = (warp - 4) >> 2;
         const int nb = (a.n + 127) / 128;
@@ -400,8 +466,12 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
         const float *sa = nullptr, *sb = nullptr;
         float sa_next = 0.f, sb_next = 0.f;
         bool live = false;
-        auto open = [&](int tile) {
-            t = decode8(tail, a.G, n_tiles, tile);
+        auto open = [&](int nth) {
+            const bool there =
+                take_tile(tail, nth, t, abort_flag, status, SITE_GEMM_EPILOGUE, limit);
+            ok = __all_sync(0xffffffffu, there);
+            if (!ok) return;
+            if (lane == 0) mbar_arrive(&tail->tile_empty[nth % kTileRing]);
             live = r < t.rows;
             sa = a.sa + t.row0 + r;
             sb = a.sb +
@@ -409,7 +479,8 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             sa_next = live ? __ldg(sa) : 0.f;
             sb_next = __ldg(sb);
         };
-        if ((int)blockIdx.x < total) open(blockIdx.x);
+        int nth = 0;
+        if ((int)blockIdx.x < total) open(nth);
         for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
             uint64_t acc[kCols / 2];
 #pragma unroll
@@ -429,18 +500,20 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
                 tc_fence_after();
                 const uint32_t ta = tmem + (uint32_t)(buf * BN + half * kCols) +
                                     ((uint32_t)(wq * 32) << 16);
-                // the next 32 columns are on their way while these are added
-                uint32_t v[2][32];
-                tmem_ld32(ta, v[0]);
+                if (wq * 32 < t.rows) {  // else none of the warp's rows exist
+                    // the next 32 columns are on their way while these are added
+                    uint32_t v[2][32];
+                    tmem_ld32(ta, v[0]);
 #pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) {
-                    tmem_ld_wait();
-                    if (c + 1 < kCols / 32) tmem_ld32(ta + 32 * (c + 1), v[(c + 1) & 1]);
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < kCols / 32) tmem_ld32(ta + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[16 * c + i] = fma_pair(pair2(__uint_as_float(v[c & 1][2 * i]),
-                                                         __uint_as_float(v[c & 1][2 * i + 1])),
-                                                   s2, acc[16 * c + i]);
+                        for (int i = 0; i < 16; ++i)
+                            acc[16 * c + i] = fma_pair(pair2(__uint_as_float(v[c & 1][2 * i]),
+                                                             __uint_as_float(v[c & 1][2 * i + 1])),
+                                                       s2, acc[16 * c + i]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -450,7 +523,7 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             // the next tile's scales are on their way while this one is stored
             const size_t row0 = (size_t)t.row0 + wq * 32;
             const int rows = t.rows - wq * 32, col0 = t.nt * BN + half * kCols;
-            if (tile + (int)gridDim.x < total) open(tile + gridDim.x);
+            if (tile + (int)gridDim.x < total) open(++nth);
             store_rows(a, stage, row0, rows, col0, lane, acc);
         }
     }
@@ -467,8 +540,10 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
 template <int BN>
 cudaError_t launch_fp8(const void* a8, const void* b8, const Fp8Args& a, cudaStream_t s) {
     Fp8Maps m;
-    if (!make_map_e4m3(&m.a, a8, (uint64_t)a.k, (uint64_t)a.R, 1, kM8, false) ||
-        !make_map_e4m3(&m.b, b8, (uint64_t)a.k, (uint64_t)a.n, (uint64_t)a.G, BN, true))
+    for (int i = 0; i < kRowBoxes; ++i)
+        if (!make_map_e4m3(&m.a[i], a8, (uint64_t)a.k, (uint64_t)a.R, 1, 32u << i, false))
+            return cudaErrorInvalidValue;
+    if (!make_map_e4m3(&m.b, b8, (uint64_t)a.k, (uint64_t)a.n, (uint64_t)a.G, BN, true))
         return cudaErrorInvalidValue;
     auto kern = fp8_gemm_kernel<BN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -515,12 +590,15 @@ MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
     f.k = k;
     f.out_f32 = out_dt == MOE_F32 ? 1 : 0;
     f.y = y;
+    f.wide_rows = n % 16 == 0 && aligned(y, 32);
     f.status = static_cast<int*>(status_ws);
     f.wait_limit_ns = kWaitLimitNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // the widest tile that still gives every SM one
+    // the widest tile that still gives every SM one; groups of few rows, where
+    // the weights' bytes count and not the products, take the second (64 experts
+    // of 6 rows: 47 us against 51, tiles come out more even)
     const long long rows_tiles = std::max((long long)std::min(G, R), ((long long)R + kM8 - 1) / kM8);
-    if (rows_tiles * ((n + 255) / 256) >= num_sms()) return ret(launch_fp8<256>(a, b, f, s));
+    if (R > 64LL * G && rows_tiles * ((n + 255) / 256) >= num_sms()) return ret(launch_fp8<256>(a, b, f, s));
     if (rows_tiles * ((n + 127) / 128) >= num_sms()) return ret(launch_fp8<128>(a, b, f, s));
     return ret(launch_fp8<64>(a, b, f, s));
 }
