@@ -43,6 +43,7 @@ struct Fp8Args {
     const int32_t* counts;  // nullptr: one group of R rows
     int R, G, n, k;
     int out_f32;
+    int split;      // CTAs per tile (split launches)
     int wide_rows;  // rows of y are 32-byte aligned
     void* y;
     int* status;
@@ -182,6 +183,29 @@ __device__ __forceinline__ Tile8 decode8(const TAIL* t, int G, int n_tiles, int 
     return r;
 }
 
+// Four columns of a row.
+__device__ __forceinline__ void store4(const Fp8Args& a, size_t row, int col, const float4& v) {
+    const size_t at = row * (size_t)a.n + col;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    if (a.n % 4 == 0) {
+        if (col >= a.n) return;
+        if (a.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v;
+        else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + i >= a.n) return;
+        if (a.out_f32)
+            static_cast<float*>(a.y)[at + i] = f[i];
+        else
+            static_cast<__nv_bfloat16*>(a.y)[at + i] = __float2bfloat16_rn(f[i]);
+    }
+}
+
 // Columns col .. col + 2 W - 1 of the warp's 32 rows (lane = row; `rows` of them
 // exist) from sums in registers.  A lane's 64 bytes at a time go through the
 // warp's staging rows (16-byte chunk q of row r at q ^ (r / 2 % 4): both sides
@@ -281,11 +305,31 @@ __device__ __forceinline__ void store_rows(const Fp8Args& a, uint4* stage, size_
     }
 }
 
-template <int BN>
+// Split launches (few row tiles and a long reduction): a cluster of S CTAs takes
+// one tile, each a part of the blocks, and they add their fp32 sums over
+// distributed shared memory, in rank order.
+constexpr int kMaxSplit = 8;
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+__device__ __forceinline__ float4 ld_rank(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .u32 p;\n\tmapa.shared::cluster.u32 p, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
     const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Args a) {
     using SH = Shape8<BN>;
     constexpr int kStages = SH::kStages;
+    constexpr int kPartRow = BN / 4 + 1;  // float4 per row of sums: no bank conflicts
     extern __shared__ uint8_t raw8[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw8) + 1023) &
                                                ~(uintptr_t)1023);
@@ -364,6 +408,12 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
     const int n_tiles = (a.n + BN - 1) / BN;
     const int total = tail->tile_off[a.G] * n_tiles;
     const int kb_n = (a.k + kK8 - 1) / kK8;
+    // tiles first_tile, first_tile + step, .. of this CTA, blocks [kb0, kb1) of each
+    const int S = SPLIT ? a.split : 1;
+    const int rank = SPLIT ? (int)blockIdx.x % S : 0;
+    const int first_tile = SPLIT ? (int)blockIdx.x / S : (int)blockIdx.x;
+    const int step = SPLIT ? 1 << 30 : (int)gridDim.x;  // split: one tile
+    const int kb0 = rank * kb_n / S, kb1 = (rank + 1) * kb_n / S;
 
     if (warp < 4) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
@@ -374,14 +424,14 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             uint32_t ph = 0, issued = 0, issued_ph = 0;
             bool ok = true;
             int nth = 0;
-            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++nth) {
+            for (int tile = first_tile; tile < total && ok; tile += step, ++nth) {
                 Tile8 t;
                 ok = take_tile(tail, nth, t, abort_flag, status, SITE_GEMM_PRODUCER, limit);
                 if (!ok) break;
                 mbar_arrive(&tail->tile_empty[nth % kTileRing]);
                 const int box = t.rows <= 32 ? 0 : t.rows <= 64 ? 1 : 2;
                 const uint32_t bytes = (uint32_t)((32 << box) * kK8 + BN * kK8);
-                for (int kb = 0; kb < kb_n; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = mbar_wait_bounded(&tail->empty[s], ph ^ 1u, abort_flag, status,
                                            SITE_GEMM_PRODUCER, limit);
                     if (!ok) break;
@@ -412,8 +462,8 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             const uint64_t ad0 = sw128_kmajor_desc(smem_u32(smem));
             const uint64_t bd0 = sw128_kmajor_desc(smem_u32(smem) + kABytes8);
             constexpr uint32_t idesc = idesc_e4m3_f32(kM8, BN);
-            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                for (int kb = 0; kb < kb_n; ++kb, ++blk) {
+            for (int tile = first_tile; tile < total && ok; tile += step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++blk) {
                     const int buf = blk & 1;
                     ok = mbar_wait_bounded(&tail->tempty[buf], ((blk >> 1) & 1) ^ 1u, abort_flag,
                                            status, SITE_GEMM_MMA, limit) &&
@@ -439,7 +489,7 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
         // ------------------------------------------------ tiles, decoded
         if (lane == 0) {
             int nth = 0;
-            for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++nth) {
+            for (int tile = first_tile; tile < total; tile += step, ++nth) {
                 const Tile8 t = decode8(tail, a.G, n_tiles, tile);
                 const int slot = nth % kTileRing;
                 if (!mbar_wait_bounded(&tail->tile_empty[slot], ((nth / kTileRing) & 1) ^ 1u,
@@ -476,19 +526,19 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
             sa = a.sa + t.row0 + r;
             sb = a.sb +
                  ((size_t)t.g * nb + min((t.nt * BN + half * kCols) / 128, nb - 1)) * kb_n;
-            sa_next = live ? __ldg(sa) : 0.f;
-            sb_next = __ldg(sb);
+            sa_next = live ? __ldg(sa + (size_t)kb0 * a.R) : 0.f;
+            sb_next = __ldg(sb + kb0);
         };
         int nth = 0;
-        if ((int)blockIdx.x < total) open(nth);
-        for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        if (first_tile < total) open(nth);
+        for (int tile = first_tile; tile < total && ok; tile += step) {
             uint64_t acc[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
-            for (int kb = 0; kb < kb_n; ++kb, ++blk) {
+            for (int kb = kb0; kb < kb1; ++kb, ++blk) {
                 const float sc = sa_next * sb_next;
                 const uint64_t s2 = pair2(sc, sc);
-                if (kb + 1 < kb_n) {
+                if (kb + 1 < kb1) {
                     sa_next = live ? __ldg(sa + (size_t)(kb + 1) * a.R) : 0.f;
                     sb_next = __ldg(sb + kb + 1);
                 }
@@ -520,12 +570,50 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
                 if (lane == 0) mbar_arrive(&tail->tempty[buf]);
             }
             if (!ok) break;
+            if (SPLIT) {
+                // all of this CTA's products are done: the ring is free for its sums
+                float4* part = reinterpret_cast<float4*>(smem) + r * kPartRow + half * (kCols / 4);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < kCols / 4; ++i) {
+                        const float2 u = unpair(acc[2 * i]), v = unpair(acc[2 * i + 1]);
+                        part[i] = make_float4(u.x, u.y, v.x, v.y);
+                    }
+                }
+                break;
+            }
             // the next tile's scales are on their way while this one is stored
             const size_t row0 = (size_t)t.row0 + wq * 32;
             const int rows = t.rows - wq * 32, col0 = t.nt * BN + half * kCols;
-            if (tile + (int)gridDim.x < total) open(++nth);
+            if (tile + step < total) open(++nth);
             store_rows(a, stage, row0, rows, col0, lane, acc);
         }
+    }
+    if (SPLIT) {
+        __syncthreads();
+        cluster_meet();
+        // this CTA's share of the tile's rows, 4 columns per thread
+        if (first_tile < total && !*abort_flag) {
+            const int m_tiles = tail->tile_off[1];
+            const int row0 = first_tile % m_tiles * kM8, col0 = first_tile / m_tiles * BN;
+            const int rows = min(kM8, a.R - row0);
+            const int r0 = rank * rows / S, r1 = (rank + 1) * rows / S;
+            for (int i = threadIdx.x; i < (r1 - r0) * (BN / 4); i += kThreads8) {
+                const int r = r0 + i / (BN / 4), c = i % (BN / 4);
+                const uint32_t at = smem_u32(smem) + (uint32_t)(r * kPartRow + c) * 16;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int q = 0; q < S; ++q) {
+                    const float4 o = ld_rank(at, (uint32_t)q);
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                store4(a, (size_t)(row0 + r), col0 + 4 * c, v);
+            }
+        }
+        cluster_meet();  // no CTA leaves while another reads its sums
     }
     pdl_trigger();
     tc_fence_before();
@@ -537,20 +625,22 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
                      : "memory");
 }
 
-template <int BN>
-cudaError_t launch_fp8(const void* a8, const void* b8, const Fp8Args& a, cudaStream_t s) {
+// split == 1: persistent, one CTA per SM; else clusters of split CTAs, one per tile
+template <int BN, bool SPLIT = false>
+cudaError_t launch_fp8(const void* a8, const void* b8, const Fp8Args& a, cudaStream_t s,
+                       int tiles = 0) {
     Fp8Maps m;
     for (int i = 0; i < kRowBoxes; ++i)
         if (!make_map_e4m3(&m.a[i], a8, (uint64_t)a.k, (uint64_t)a.R, 1, 32u << i, false))
             return cudaErrorInvalidValue;
     if (!make_map_e4m3(&m.b, b8, (uint64_t)a.k, (uint64_t)a.n, (uint64_t)a.G, BN, true))
         return cudaErrorInvalidValue;
-    auto kern = fp8_gemm_kernel<BN>;
+    auto kern = fp8_gemm_kernel<BN, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem_bytes8<BN>());
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)num_sms()), dim3(kThreads8), smem_bytes8<BN>(), s, 1, m,
-                      a);
+    const unsigned grid = SPLIT ? (unsigned)(tiles * a.split) : (unsigned)num_sms();
+    return launch_pdl(kern, dim3(grid), dim3(kThreads8), smem_bytes8<BN>(), s, a.split, m, a);
 }
 
 }  // namespace
@@ -590,6 +680,7 @@ MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
     f.k = k;
     f.out_f32 = out_dt == MOE_F32 ? 1 : 0;
     f.y = y;
+    f.split = 1;
     f.wide_rows = n % 16 == 0 && aligned(y, 32);
     f.status = static_cast<int*>(status_ws);
     f.wait_limit_ns = kWaitLimitNs;
@@ -600,6 +691,15 @@ MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
     const long long rows_tiles = std::max((long long)std::min(G, R), ((long long)R + kM8 - 1) / kM8);
     if (R > 64LL * G && rows_tiles * ((n + 255) / 256) >= num_sms()) return ret(launch_fp8<256>(a, b, f, s));
     if (rows_tiles * ((n + 127) / 128) >= num_sms()) return ret(launch_fp8<128>(a, b, f, s));
+    // One group with few tiles and a long reduction: several CTAs per tile, at
+    // least 4 blocks each (64 rows, n 2048, k 6144: 10.7 us by 4 CTAs per tile, 22.5
+    // by one).
+    const long long tiles = (((long long)R + kM8 - 1) / kM8) * ((n + 63) / 64);
+    const int kb_n = (k + kK8 - 1) / kK8;
+    while (counts == nullptr && f.split < kMaxSplit && 2 * f.split * tiles <= num_sms() &&
+           kb_n >= 8 * f.split)
+        f.split *= 2;
+    if (f.split > 1) return ret(launch_fp8<64, true>(a, b, f, s, (int)tiles));
     return ret(launch_fp8<64>(a, b, f, s));
 }
 

@@ -192,7 +192,10 @@ def check_product(y, want, mag, k, fill=None):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("R,n,k", [(1, 1, 16), (1, 2048, 1536), (3, 100, 144), (64, 257, 256),
                                    (128, 128, 128), (129, 320, 400), (500, 1000, 1040),
-                                   (2000, 2050, 272)])
+                                   (2000, 2050, 272),
+                                   # several CTAs per tile
+                                   (64, 2048, 6144), (5, 100, 4096), (200, 66, 2064),
+                                   (1, 129, 16400), (128, 1000, 1104)])
 def test_dense_product(R, n, k, out):
     a, sa, b, sb = operands(R, 1, n, k, seed=R + n + k)
     y = moe.matmul_fp8(a, sa, b[0], sb[0], out_dtype=DT[out])
