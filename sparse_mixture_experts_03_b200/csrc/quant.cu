@@ -32,7 +32,7 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr int kQuantRows = 8;         // rows per CTA: 8 scales of a block column are one 32-byte piece
 constexpr float kE4m3Max = 448.f;
-constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
+constexpr uint32_t kAmaxFloorBits = 27u << 23;  // 2^-100
 
 // How one block is quantised: t = x * mul * r, corrected with A = den.
 struct BlockScale {
@@ -46,11 +46,8 @@ struct BlockScale {
 // or above 0x7f800000, so an integer maximum keeps them
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
     BlockScale b;
-    if (amax_bits >= 0x7f800000u) {
-        b.scale = b.mul = b.den = b.rcp = __uint_as_float(0x7fffffffu);
-        return b;
-    }
-    const float A = fmaxf(__uint_as_float(amax_bits), kAmaxFloor);
+    amax_bits = amax_bits >= 0x7f800000u ? 0x7fffffffu : max(amax_bits, kAmaxFloorBits);
+    const float A = __uint_as_float(amax_bits);
     const float pre = A > 1.2676506e30f ? 9.5367431640625e-07f : 1.f;  // above 2^100: 2^-20
     // A / 448, rounded once: a product with 1 / 448 and its correction (all
     // lanes of a block do this: a division would be a tenth of the kernel)
@@ -62,15 +59,37 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
     return b;
 }
 
-__device__ __forceinline__ float quotient(float x, const BlockScale& b) {
-    const float n = x * b.mul;
-    const float t = n * b.rcp;
-    return fmaf(fmaf(-t, b.den, n), b.rcp, t);
+// Pairs of fp32 values: one instruction for two of them (the kernels are bound
+// by the instructions they issue).
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The quotients of two values: t = n rcp, corrected by (n - t den) rcp.
+__device__ __forceinline__ float2 quotients(float x, float y, const BlockScale& b) {
+    const uint64_t r = pair_of(b.rcp, b.rcp);
+    const uint64_t n = mul_pair(pair_of(x, y), pair_of(b.mul, b.mul));
+    const uint64_t t = mul_pair(n, r);
+    const uint64_t q = fma_pair(fma_pair(t, pair_of(-b.den, -b.den), n), r, t);
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(q));
+    return f;
 }
 
 // The fp32 input's quotient, on the right side of every border (see above).
-__device__ __forceinline__ float quotient_f32(float x, const BlockScale& b) {
-    const float t = quotient(x, b);
+__device__ __forceinline__ float settle_f32(float x, float t, const BlockScale& b) {
     const uint32_t u = __float_as_uint(t) & 0x7fffffffu;
     const uint32_t off = (u & 0xfffffu) - 0x7fffcu;  // low 20 bits within 4 of 0x80000: 0..8
     if (__builtin_expect(u >= 0x3c800000u && off > 8u, 1)) return t;  // 0x3c800000: 2^-6
@@ -107,8 +126,13 @@ struct Bf16x8 {
     }
     // the bits of the largest magnitude, as fp32
     __device__ __forceinline__ uint32_t amax() const {
-        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                    __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        uint32_t m;
+        asm("{\n\t.reg .b32 a, b, c, d;\n\t"
+            "abs.bf16x2 a, %1;\n\tabs.bf16x2 b, %2;\n\tabs.bf16x2 c, %3;\n\t"
+            "abs.bf16x2 d, %4;\n\tmax.NaN.bf16x2 a, a, b;\n\tmax.NaN.bf16x2 c, c, d;\n\t"
+            "max.NaN.bf16x2 %0, a, c;\n\t}"
+            : "=r"(m)
+            : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
         return max(m & 0xffff0000u, m << 16);
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -149,7 +173,11 @@ template <bool EXACT>
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], const BlockScale& b) {
     float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = EXACT ? quotient_f32(f[i], b) : quotient(f[i], b);
+    for (int i = 0; i < 8; i += 2) {
+        const float2 q = quotients(f[i], f[i + 1], b);
+        t[i] = EXACT ? settle_f32(f[i], q.x, b) : q.x;
+        t[i + 1] = EXACT ? settle_f32(f[i + 1], q.y, b) : q.y;
+    }
     return make_uint2(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]));
 }
 
