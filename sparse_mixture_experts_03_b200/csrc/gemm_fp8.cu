@@ -656,9 +656,10 @@ MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
     if (R < 0 || G < 1 || G > kMaxE || n <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
     if (out_dt != MOE_F32 && out_dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
     if (counts == nullptr && G != 1) return MOE_ERR_INVALID_ARG;
-    // tiles are numbered in 32 bits; TMA coordinates are 32-bit
+    // tiles are numbered in 32 bits, with room for a step behind the last
     const long long m_tiles = ((long long)R + kM8 - 1) / kM8 + G;
-    if (k % 16 != 0 || m_tiles * (((long long)n + 63) / 64) > INT_MAX) return MOE_ERR_UNSUPPORTED;
+    if (k % 16 != 0 || m_tiles * (((long long)n + 63) / 64) > (1LL << 30))
+        return MOE_ERR_UNSUPPORTED;
     if (R == 0) return MOE_OK;
     const void* p16[] = {a, b, y};
     for (const void* p : p16)

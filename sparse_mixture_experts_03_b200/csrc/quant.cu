@@ -217,7 +217,20 @@ struct SwigluSrc {
         g.get(a);
         u.get(b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = __fdividef(a[i], 1.f + __expf(-a[i])) * b[i];
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t gg = pair_of(a[i], a[i + 1]);
+            float2 e;  // exp(-g) = 2^(-g log2(e)), then 1 / (1 + it)
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(e.x), "=f"(e.y)
+                : "l"(mul_pair(gg, pair_of(-1.4426950408889634f, -1.4426950408889634f))));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+            e.x += 1.f;
+            e.y += 1.f;
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(h[i]), "=f"(h[i + 1])
+                : "l"(mul_pair(mul_pair(gg, pair_of(e.x, e.y)), pair_of(b[i], b[i + 1]))));
+        }
     }
     __device__ __forceinline__ uint32_t amax() const { return amax_bits8(h); }
     __device__ __forceinline__ void get(float (&f)[8]) const {

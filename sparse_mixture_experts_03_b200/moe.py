@@ -495,6 +495,14 @@ def _on_current(name: str, t: torch.Tensor, stream) -> Tuple[int, int]:
                           else stream.cuda_stream)
 
 
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated here for work on another stream than the current one:
+    their memory is not handed out again before that work is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _blocks(n: int) -> int:
     return (n + 127) // 128
 
@@ -523,6 +531,7 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     st = lib().moe_quantize_rows(px, R, d, dt, pq, ps, s)
     if st:
         _check(st, "moe_quantize_rows")
+    _used_on(stream, q, scales)
     return q, scales
 
 
@@ -553,6 +562,7 @@ def swiglu_quantize_rows(gate_up: torch.Tensor, w: Optional[torch.Tensor] = None
     st = lib().moe_swiglu_quantize_rows(px, pw, R, inter, dt, pq, ps, s)
     if st:
         _check(st, "moe_swiglu_quantize_rows")
+    _used_on(stream, q, scales)
     return q, scales
 
 
@@ -581,6 +591,7 @@ def quantize_weight(W: torch.Tensor, q: Optional[torch.Tensor] = None,
     st = lib().moe_quantize_weight(px, G, n, k, dt, pq, ps, s)
     if st:
         _check(st, "moe_quantize_weight")
+    _used_on(stream, q, scales)
     return q, scales
 
 
@@ -614,6 +625,7 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
                               s)
     if st:
         _check(st, "moe_matmul_fp8")
+    _used_on(stream, y)
     return y
 
 
@@ -682,6 +694,7 @@ def forward_few(x: torch.Tensor, W_router: torch.Tensor, W_gate_up: torch.Tensor
                                pi, pw, pws, workspace.numel(), s)
     if st:
         _check(st, "moe_forward_few")
+    _used_on(stream, y, workspace)
     return y
 
 

@@ -21,6 +21,9 @@ SHAPES = [
     (16, 256, 4, 4, 1, 1, 1152, 0),      # every expert takes every token
     (5, 1280, 256, 8, 32, 8, 128, 1),    # many experts, an odd number of row pieces
     (2, 2048, 64, 6, 8, 4, 1536, 4),     # the workloads' layer
+    (3, 4096, 4, 2, 1, 1, 2304, 1),      # rows longer than one pass makes operand B of
+    (11, 2560, 6, 3, 3, 2, 2688, 0),
+    (8, 7168, 2, 1, 1, 1, 128, 0),       # the least room for the ring
 ]
 
 
@@ -201,3 +204,38 @@ def test_graph_and_two_streams(fp8):
         torch.cuda.synchronize()
         assert torch.equal(y, a.run()[0])
     del g
+
+
+def test_side_stream_without_a_workspace():
+    """What the call allocates for work on another stream is not reused before
+    that work is done."""
+    layer = Layer((4, 512, 32, 6, 4, 2, 256, 2), False, seed=1)
+    want = layer.run()[0]
+    s = torch.cuda.Stream()
+    n = moe.few_workspace_bytes(4, 512, 32, 6, 256, 2)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(1000000)  # the call starts later than what follows here
+        y = layer.run(stream=s)[0]
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del junk
+
+
+def test_refusals_on_the_gpu():
+    layer = Layer((4, 256, 16, 4, 4, 2, 128, 1), False)
+    with pytest.raises(TypeError):
+        layer.run(scales=(layer.Wr.float(), layer.Wr.float(), None))  # 16-bit weights, scales
+    with pytest.raises(ValueError):
+        layer.run(y=torch.empty(4, 255, device=DEV))
+    with pytest.raises(ValueError):
+        moe.forward_few(layer.x.cpu(), layer.Wr, layer.gu, layer.dn, layer.sh, 4, 4, 2, 128, 1)
+    with pytest.raises(ValueError):
+        moe.forward_few(layer.x[:, ::2], layer.Wr, layer.gu, layer.dn, layer.sh, 4, 4, 2, 128, 1)
+    with pytest.raises(moe.MoeError):
+        layer.run(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    x17 = torch.zeros(17, 256, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(moe.MoeError):
+        moe.forward_few(x17, layer.Wr, layer.gu, layer.dn, layer.sh, 4, 4, 2, 128, 1)

@@ -280,6 +280,48 @@ def test_product_on_a_side_stream_and_in_a_graph():
     del g
 
 
+def test_refusals_on_the_gpu():
+    a, sa, b, sb = operands(8, 2, 32, 128)
+    c = torch.tensor([4, 4], dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError):
+        moe.matmul_fp8(randn(8, 128), sa, b, sb, c)
+    with pytest.raises(ValueError):
+        moe.matmul_fp8(a, sa.t().contiguous(), b, sb, c)        # scales lie [block][row]
+    with pytest.raises(TypeError):
+        moe.matmul_fp8(a, sa, b, sb, c.long())
+    with pytest.raises(ValueError):
+        moe.matmul_fp8(a, sa, b, sb, c[:1])
+    with pytest.raises(moe.MoeError):
+        moe.matmul_fp8(a, sa, b, sb)                            # two groups without counts
+    with pytest.raises(ValueError):
+        moe.matmul_fp8(a, sa, b, sb, c, status_ws=torch.zeros(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(TypeError):
+        moe.matmul_fp8(a, sa, b, sb, c, out_dtype=torch.float16)
+    with pytest.raises(moe.MoeError):
+        moe.quantize_rows(randn(4, 24))                         # d % 16
+    with pytest.raises(ValueError):
+        moe.quantize_rows(randn(4, 256)[:, :128])               # not contiguous
+    base = torch.zeros(4 * 128 + 8, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(moe.MoeError):
+        moe.quantize_rows(base[4:4 + 512].view(4, 128))         # 8-byte aligned rows
+
+
+def test_offsets_beyond_32_bits():
+    """Rows and codes whose byte offsets pass 2^32, from the last rows."""
+    R, d = 1_100_000, 2048  # 4.5 GB of bf16, 2.25 GB of codes
+    x = torch.zeros(R, d, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = randn(3, d, seed=1)
+    q, s = moe.quantize_rows(x)
+    want_q, want_s = row_blocks(x[-3:].double())
+    assert torch.equal(q[-3:].double(), want_q) and scales_equal(s[:, -3:], want_s)
+    del x
+    b, sb = moe.quantize_weight(randn(1, 2064, d, seed=2))  # y: 2.27e9 values
+    y = moe.matmul_fp8(q, s, b[0], sb[0])
+    want, mag = product64(q[-3:], s[:, -3:].contiguous(), b, sb, [3])
+    check_product(y[-3:], want, mag, d)
+    assert not y[:128].any()
+
+
 # ---------------------------------------------------------------- the layer on 8-bit weights
 
 def fp8_layer(E=16, k=4, G=4, TG=2, d=512, I=256, S=2, seed=0, **kw):
