@@ -1076,14 +1076,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         fence_barrier_init();
     }
     __syncthreads();
+    pdl_trigger();  // the next kernel waits for this one's end by itself
     if (warp < kWarps)
         products<NT, FP8>(a, s, warp, lane);
     else if (warp < kWarps + kSumWarps)
         sums<NT>(a, s, warp - kWarps, lane);
     else
         producer<FP8>(a, s, lane);
-    __syncthreads();
-    pdl_trigger();
 }
 
 // ---------------------------------------------------------------- host

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
         fence_barrier_init();
     }
     pdl_wait();
+    pdl_trigger();  // the next kernel waits for this one's end by itself
     if (warp == 0) {
         // rows and row tiles of each group (exclusive prefix sums), cut at R rows
         int rows = 0, tiles = 0;
@@ -615,7 +616,6 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
         }
         cluster_meet();  // no CTA leaves while another reads its sums
     }
-    pdl_trigger();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
     const int rows = min(kQuantRows, R - r0);
     const int chunks = (d + 255) / 256;
     pdl_wait();
+    pdl_trigger();  // the next kernel waits for this one's end by itself
     // the next chunk of this warp, 8 further on each time (no division per chunk)
     const int step_row = 8 / chunks, step_ch = 8 - step_row * chunks;
     int row_n = warp / chunks, ch_n = warp - row_n * chunks;
@@ -299,7 +300,6 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
         const int row = i % kQuantRows;
         if (row < rows) scales[(size_t)(i / kQuantRows) * R + r0 + row] = s_scale[i];
     }
-    pdl_trigger();
 }
 
 // Weights.  CTA: one 128 x 128 block held in registers (8 columns x 8 rows per
@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weight_kernel(
     const size_t g = blk / ((size_t)kb * nb);
     const int col = bk * 128 + (tid & 15) * 8, row0 = bn * 128 + (tid >> 4);
     pdl_wait();
+    pdl_trigger();  // the next kernel waits for this one's end by itself
     V v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -342,7 +343,6 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_weight_kernel(
         }
     }
     if (tid == 0) scales[blk] = b.scale;
-    pdl_trigger();
 }
 
 // One row's scales have to fit the kernel's default shared memory.

@@ -192,7 +192,7 @@ def check_product(y, want, mag, k, fill=None):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("R,n,k", [(1, 1, 16), (1, 2048, 1536), (3, 100, 144), (64, 257, 256),
                                    (128, 128, 128), (129, 320, 400), (500, 1000, 1040),
-                                   (2000, 2050, 272),
+                                   (2000, 2050, 272), (5001, 2048, 400), (9000, 1001, 272),
                                    # several CTAs per tile
                                    (64, 2048, 6144), (5, 100, 4096), (200, 66, 2064),
                                    (1, 129, 16400), (128, 1000, 1104)])
@@ -211,6 +211,9 @@ def test_dense_product(R, n, k, out):
     ([1] * 200, 72, 96, 200),                    # many groups of one row
     ([3, -4, 2], 40, 64, 5),                     # a negative count is an empty group
     ([700, 1, 33], 1300, 512, 734),
+    # CTA pairs: 256-row tiles, some with rows of the first CTA only
+    ([1000, 0, 300, 2000, 57, 1500], 2100, 144, 5000),
+    ([256, 1, 128, 4000, 129, 700, 2], 2050, 272, 5216),
 ])
 def test_grouped_product(counts, n, k, R):
     a, sa, b, sb = operands(R, len(counts), n, k, seed=R)
