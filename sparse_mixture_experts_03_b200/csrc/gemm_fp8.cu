@@ -14,10 +14,19 @@
 // CTA (one per SM, persistent): 128 rows x BN columns.  Warp 0 loads the
 // operands by TMA (128-byte swizzle) into a ring of stages, warp 1 issues the
 // products, warp 2 decodes tiles ahead of them (a search and two divisions, 1 us
-// per tile in the adding warps), warps 4..11 add (two warps per SM sub-partition: TMEM lanes
-// 32 (w % 4).., columns half (w - 4) / 4).  128 sums a thread need more
-// registers than an even split leaves: warps 0..3 hand theirs over (of the
-// launch's 384 x 168, 128 x 120 + 256 x 192).
+// per tile in the adding warps), warps 4..11 add (two warps per SM
+// sub-partition: TMEM lanes 32 (w % 4).., columns half (w - 4) / 4).  128 sums a
+// thread need more registers than an even split leaves: warps 0..3 hand some of
+// theirs over (of the launch's 384 x 168, 128 x 120 + 256 x 192; with 128 x 56 the
+// issuing warps spilled and the kernel took a quarter longer).
+//
+// Many rows (24576 rows in 64 uneven groups, n 2048, k 1536: 130 us, 1.19
+// PFLOP/s): bound by shared memory, 96 bytes a clock written and 96 read per
+// block of 512 clocks, about 870 clocks a block.  A pair of CTAs on one 256-row
+// tile moves two thirds of that, but its accumulators are released across the
+// two SMs, and with the two that TMEM holds it waited for that: 139 us.  Few
+// rows (384 rows in 64 groups: 46 us): the weights, at 6.4 TB/s once the first
+// tile has arrived; 7 tiles for some CTAs and 6 for others.
 #include <cudaTypedefs.h>
 #include <limits.h>
 
