@@ -301,16 +301,14 @@ __device__ __forceinline__ void sums_sync() {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -359,9 +357,10 @@ template <int NT>
 __host__ __device__ constexpr int red_bytes() {
     return kSumBufs * kWarps * NT * 32 * 16;
 }
-constexpr int kSmallBytes = 1024 + kMaxStages * (32 * 4 + 16 + 16) + 64 + kSumWarps * 24 + kSumBufs * 8 +
-                            kFewMaxT * 4 + kFewMaxT * kMaxK * 8 + kMaxE * 4 + kMaxEntries * 4 +
-                            kSumWarps * kMaxE * 4 + 64;
+// everything else in shared memory (1024: the ring's alignment)
+constexpr int kSmallBytes = 1024 + kMaxStages * (32 * 4 + 16 + 16) + 64 + kSumWarps * 24 +
+                            kSumBufs * 8 + kFewMaxT * 4 + kFewMaxT * kMaxK * 8 + kMaxE * 4 +
+                            kMaxEntries * 4 + kSumWarps * kMaxE * 4 + 64;
 
 template <int NT>
 __host__ __device__ inline int b_bytes(int d, int I) {
@@ -856,7 +855,7 @@ __device__ __forceinline__ void products(const FewArgs& a, const Smem& s, int wa
             bool ok = mbar_wait_bounded(s.routed, 0, s.abort, a.status, SITE_GEMM_EPILOGUE,
                                         a.wait_limit_ns);  // the entry list: long there
             ok = ok && wait_count(a.ctrl + kCtrlH + entry, I / 8, s.abort, a.status,
-                                       SITE_GEMM_BOUNDS, a.wait_limit_ns);
+                                  SITE_GEMM_BOUNDS, a.wait_limit_ns);
             if (!__all_sync(0xffffffffu, ok)) return;
             const uint32_t mask = entry < S ? all : s.s_mask[s.list[entry]];
             fill_b<NT, FP8>(s, a.h + (size_t)entry * T * I, I, I, mask, T, false, warp, lane);
@@ -966,7 +965,7 @@ __device__ __forceinline__ void sums(const FewArgs& a, const Smem& s, int who, i
         if (!__all_sync(0xffffffffu, filled)) return;
         const int4 info = s.unit[who];
         const int buf = unit % kSumBufs;
-            const float4* red = s.red + buf * kWarps * NT * 32 + lane;
+        const float4* red = s.red + buf * kWarps * NT * 32 + lane;
         float4 sum[NT];
         if (info.x == WHAT_UP || info.x == WHAT_DOWN) {
 #pragma unroll

@@ -20,13 +20,13 @@
 // theirs over (of the launch's 384 x 168, 128 x 120 + 256 x 192; with 128 x 56 the
 // issuing warps spilled and the kernel took a quarter longer).
 //
-// Many rows (24576 rows in 64 uneven groups, n 2048, k 1536: 130 us, 1.19
+// Many rows (24576 rows in 64 uneven groups, n 2048, k 1536: 128 us, 1.2
 // PFLOP/s): bound by shared memory, 96 bytes a clock written and 96 read per
 // block of 512 clocks, about 870 clocks a block.  A pair of CTAs on one 256-row
 // tile moves two thirds of that, but its accumulators are released across the
 // two SMs, and with the two that TMEM holds it waited for that: 139 us.  Few
-// rows (384 rows in 64 groups: 46 us): the weights, at 6.4 TB/s once the first
-// tile has arrived; 7 tiles for some CTAs and 6 for others.
+// rows (384 rows in 64 groups: 41 us): the weights, at 6.4 TB/s once the first
+// tile has arrived; 4 tiles for some CTAs and 3 for others.
 #include <cudaTypedefs.h>
 #include <limits.h>
 
@@ -695,21 +695,30 @@ MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
     f.status = static_cast<int*>(status_ws);
     f.wait_limit_ns = kWaitLimitNs;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // the widest tile that still gives every SM one; groups of few rows, where
-    // the weights' bytes count and not the products, take the second (64 experts
-    // of 6 rows: 47 us against 51, tiles come out more even)
-    const long long rows_tiles = std::max((long long)std::min(G, R), ((long long)R + kM8 - 1) / kM8);
-    if (R > 64LL * G && rows_tiles * ((n + 255) / 256) >= num_sms()) return ret(launch_fp8<256>(a, b, f, s));
-    if (rows_tiles * ((n + 127) / 128) >= num_sms()) return ret(launch_fp8<128>(a, b, f, s));
+    // The tile width whose rounds over the SMs take least, by what a block of 128
+    // and a tile's start and end take (us, measured at d 2048, inter 1536: a
+    // block 0.73 of 256 columns, 0.40 of 128, 0.42 of 64; a tile 2).  64 rows, n
+    // 12288, k 2048: 96 tiles of 128 columns take 11.5 us, 192 of 64 columns 16.8;
+    // 1024 rows, n 2048, k 6144: 28 and 44; 384 rows in 64 groups, n 2048, k 1536:
+    // 256 columns 41, 128 columns 46, 64 columns 76.  How many row tiles the groups make is on the device: one each, or R / 128.
+    const long long row_tiles =
+        std::max((long long)std::min(G, R), ((long long)R + kM8 - 1) / kM8);
+    const int kb_n = (k + kK8 - 1) / kK8, sms = num_sms();
+    auto cost = [&](int bn, double block) {
+        const long long tiles = row_tiles * (((long long)n + bn - 1) / bn);
+        return (double)((tiles + sms - 1) / sms) * (kb_n * block + 2.0);
+    };
     // One group with few tiles and a long reduction: several CTAs per tile, at
-    // least 4 blocks each (64 rows, n 2048, k 6144: 10.7 us by 4 CTAs per tile, 22.5
+    // least 4 blocks each (64 rows, n 2048, k 6144: 10.5 us by 4 CTAs per tile, 22.5
     // by one).
-    const long long tiles = (((long long)R + kM8 - 1) / kM8) * ((n + 63) / 64);
-    const int kb_n = (k + kK8 - 1) / kK8;
-    while (counts == nullptr && f.split < kMaxSplit && 2 * f.split * tiles <= num_sms() &&
+    const long long tiles = row_tiles * (((long long)n + 63) / 64);
+    while (counts == nullptr && f.split < kMaxSplit && 2 * f.split * tiles <= sms &&
            kb_n >= 8 * f.split)
         f.split *= 2;
     if (f.split > 1) return ret(launch_fp8<64, true>(a, b, f, s, (int)tiles));
+    const double c256 = cost(256, 0.73), c128 = cost(128, 0.40), c64 = cost(64, 0.42);
+    if (c256 <= c128 && c256 <= c64) return ret(launch_fp8<256>(a, b, f, s));
+    if (c128 <= c64) return ret(launch_fp8<128>(a, b, f, s));
     return ret(launch_fp8<64>(a, b, f, s));
 }
 

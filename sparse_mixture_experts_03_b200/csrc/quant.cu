@@ -23,12 +23,14 @@
 //
 // The kernels read and write each value once.  What bounds them is the number
 // of instructions they issue, then the memory: rows of d 2048 (24576 of them)
-// 29.1 us, 5.2 TB/s; SwiGLU rows (24581 of inter 1536) 34 us, 5.6 TB/s; weights
+// 30 us, 5.1 TB/s; SwiGLU rows (24581 of inter 1536) 34 us, 5.6 TB/s; weights
 // (64 x 2048 x 1536) 96.8 us, 6.2 TB/s, of 6.55 that a copy reaches.  Loading one
 // batch ahead, deeper or shallower batches, and 16 rows per CTA made no
 // difference or were slower.
 #include <cuda_fp8.h>
 #include <limits.h>
+
+#include <algorithm>
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
@@ -248,13 +250,15 @@ struct SwigluSrc {
 
 template <typename SRC, int UNROLL>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
-    const void* __restrict__ x, const float* __restrict__ w, int R, int d, int n_blocks,
+    const void* __restrict__ x, const float* __restrict__ w, int R, int d, int n_blocks, int cut,
     uint8_t* __restrict__ q, float* __restrict__ scales) {
     extern __shared__ float s_scale[];  // [n_blocks][8]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r0 = blockIdx.x * kQuantRows;
     const int rows = min(kQuantRows, R - r0);
-    const int chunks = (d + 255) / 256;
+    // this CTA's 256-column chunks of the rows (few rows are cut across CTAs)
+    const int ch0 = (int)blockIdx.y * cut;
+    const int chunks = min(cut, (d + 255) / 256 - ch0);
     pdl_wait();
     pdl_trigger();  // the next kernel waits for this one's end by itself
     // the next chunk of this warp, 8 further on each time (no division per chunk)
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i) {
             rows_i[i] = row_n;
-            cols_i[i] = row_n < rows ? ch_n * 256 + lane * 8 : d;  // d: nothing there
+            cols_i[i] = row_n < rows ? (ch0 + ch_n) * 256 + lane * 8 : d;  // d: nothing there
             row_n += step_row;
             ch_n += step_ch;
             if (ch_n >= chunks) {
@@ -297,15 +301,16 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(
                 *reinterpret_cast<uint2*>(q + (size_t)(r0 + row) * d + col) =
                     codes8<SRC::kExact>(f, b);
                 if ((lane & 15) == 0)
-                    s_scale[(col >> 7) * kQuantRows + row] =
+                    s_scale[((col >> 7) - 2 * ch0) * kQuantRows + row] =
                         w != nullptr ? b.scale * w[r0 + row] : b.scale;
             }
         }
     }
     __syncthreads();
-    for (int i = tid; i < n_blocks * kQuantRows; i += kQuantThreads) {
+    const int blk0 = 2 * ch0, blks = min(n_blocks - blk0, 2 * chunks);
+    for (int i = tid; i < blks * kQuantRows; i += kQuantThreads) {
         const int row = i % kQuantRows;
-        if (row < rows) scales[(size_t)(i / kQuantRows) * R + r0 + row] = s_scale[i];
+        if (row < rows) scales[(size_t)(blk0 + i / kQuantRows) * R + r0 + row] = s_scale[i];
     }
 }
 
@@ -359,10 +364,18 @@ template <typename SRC, int UNROLL>
 cudaError_t launch_rows(const void* x, const float* w, int R, int d, void* q, float* scales,
                         cudaStream_t s) {
     const int nb = (d + 127) / 128;
+    const long long groups = ((long long)R + kQuantRows - 1) / kQuantRows;
+    // Few rows are cut along their columns until there are two CTAs per SM or a
+    // CTA's warps have one chunk each (64 rows of inter 6144: 15 us by 8 CTAs, 2.9
+    // cut).
+    const long long chunks = (d + 255) / 256, per_cta = 8 / std::min(R, kQuantRows);
+    const long long most = std::max(1LL, chunks / std::max(1LL, per_cta));
+    const long long cuts = std::min(most, std::max(1LL, 2LL * num_sms() / groups));
+    const int cut = (int)((chunks + cuts - 1) / cuts);  // chunks of a CTA
     return launch_pdl(quantize_rows_kernel<SRC, UNROLL>,
-                      dim3((unsigned)(((long long)R + kQuantRows - 1) / kQuantRows)), dim3(kQuantThreads),
-                      sizeof(float) * kQuantRows * nb, s, 1, x, w, R, d, nb,
-                      static_cast<uint8_t*>(q), scales);
+                      dim3((unsigned)groups, (unsigned)((chunks + cut - 1) / cut)),
+                      dim3(kQuantThreads), sizeof(float) * kQuantRows * 2 * cut, s, 1, x, w, R, d,
+                      nb, cut, static_cast<uint8_t*>(q), scales);
 }
 
 int check_rows(int R, int d) {

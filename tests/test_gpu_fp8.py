@@ -42,7 +42,7 @@ def scales_equal(got, want):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("R,d", [(1, 16), (1, 2048), (7, 128), (8, 144), (9, 256), (65, 2064),
-                                 (300, 1040)])
+                                 (300, 1040), (1, 196608), (3, 6144), (64, 6160)])
 def test_rows_are_exact(R, d, dt):
     x = randn(R, d, seed=R + d, dtype=torch.float32)
     x[:, ::5] *= 30
@@ -98,7 +98,7 @@ def test_rows_of_extreme_values(dt):
 
 
 @pytest.mark.parametrize("weighted", [False, True])
-@pytest.mark.parametrize("R,inter", [(1, 128), (13, 400), (130, 1536)])
+@pytest.mark.parametrize("R,inter", [(1, 128), (13, 400), (130, 1536), (20, 6160)])
 def test_swiglu_rows(R, inter, weighted):
     gu = randn(R, 2 * inter, seed=R, dtype=torch.float32) * 3
     gu[0, :inter] = -90.0                # silu underflows towards zero
@@ -195,7 +195,9 @@ def check_product(y, want, mag, k, fill=None):
                                    (2000, 2050, 272), (5001, 2048, 400), (9000, 1001, 272),
                                    # several CTAs per tile
                                    (64, 2048, 6144), (5, 100, 4096), (200, 66, 2064),
-                                   (1, 129, 16400), (128, 1000, 1104)])
+                                   (1, 129, 16400), (128, 1000, 1104),
+                                   # between the widths
+                                   (64, 6200, 512), (1024, 1100, 800), (700, 300, 2064)])
 def test_dense_product(R, n, k, out):
     a, sa, b, sb = operands(R, 1, n, k, seed=R + n + k)
     y = moe.matmul_fp8(a, sa, b[0], sb[0], out_dtype=DT[out])
@@ -356,8 +358,8 @@ def layer64(layer, x, idx, w):
     return y
 
 
-@pytest.mark.parametrize("T,S,out", [(1, 2, torch.float32), (16, 2, torch.bfloat16),
-                                     (17, 2, torch.float32), (300, 2, torch.bfloat16),
+@pytest.mark.parametrize("T,S,out", [(1, 2, torch.float32), (8, 2, torch.bfloat16),
+                                     (9, 2, torch.float32), (300, 2, torch.bfloat16),
                                      (1100, 0, torch.float32), (33, 1, torch.float32)])
 def test_layer_on_8bit_weights(T, S, out):
     layer = fp8_layer(S=S, out_dtype=out, seed=T)
@@ -366,7 +368,7 @@ def test_layer_on_8bit_weights(T, S, out):
     idx, w = moe.route(x, layer.W_router, layer.k, layer.n_group, layer.topk_group)
     ref = layer64(layer, x, idx.long(), w)
     assert y.dtype == out and y.shape == (T, 512)
-    # Up to 16 tokens only h and y are rounded, to bf16.  Above, rows are rounded
+    # Up to 8 tokens only h and y are rounded, to bf16.  Above, rows are rounded
     # to e4m3: an error spread evenly over half a step either way is at most r =
     # 2^-4 / sqrt(3) of the norm; x's reaches h through gate (|silu'| <= 1.1) and
     # up, 2.1 r, and h has its own, r.
