@@ -58,14 +58,17 @@
 // times a power of two that brings its largest magnitude to [2^14, 2^15).
 // bf16's 8 bits fit fp16's 11 down to 2^-28 of the largest magnitude, and what
 // lies below is off by at most 2^-39 of it, far less than the fp32 sums are.
-// What bounds the 8-bit layer is this conversion (it runs at 16 codes a clock
-// and SM, 0.55 us a stage that arrives in 0.73).  Not faster: shifts and masks
-// instead (90 us where this took 80 at T = 5), half and half (87), 16 product
-// warps (82), and m16n8k32 on the codes with the tokens as two e4m3 terms (86).
+// What bounds the 8-bit layer is not one of these steps: at T = 5 it takes 72 us,
+// without the products 69, without the conversions 71, without both and the
+// reads of the stage 61; a unit is one stage, and a product warp's way through it
+// (wait, reads, conversions, products, hand-over) is a chain as long as the
+// stage takes to arrive.  Not faster: shifts and masks instead of conversions
+// (90 us where this took 80), half and half (87), 16 product warps (82), and
+// m16n8k32 on the codes with the tokens as two e4m3 terms (86).
 //
 // Measured (d 2048, inter 1536, 64 experts of which 6, 4 shared; GPU time): T = 1
-// 43.9 us for 189 MB (4.3 TB/s; the floor at the copy rate is 28.9), T = 16
-// 186 us for about 1.03 GB (5.6 TB/s; 158), T = 5 on 8-bit weights 70.7 us for
+// 44.3 us for 189 MB (4.3 TB/s; the floor at the copy rate is 28.9), T = 16
+// 184 us for about 1.03 GB (5.6 TB/s; 158), T = 5 on 8-bit weights 71.2 us for
 // 273 MB (41.7).  While weights stream they come at 6.4 TB/s; the rest is the
 // logits launch and the first loads (5 us), the wait for h between the two
 // halves (2 to 4 us) and y (2 us).
@@ -704,70 +707,90 @@ __device__ __forceinline__ void fill_b(const Smem& s, const __nv_bfloat16* src, 
     }
 }
 
-// This warp's part of one stage: blocks of 128 whose number (counted over the
-// whole reduction) is the warp's modulo the number of warps.
-template <int NT, bool FP8>
-__device__ __forceinline__ void stage_mma(const uint8_t* st, const uint4* b, const float* scales,
-                                          int k0, int len, bool up, int warp, int lane,
-                                          float (&acc)[NT][4]) {
-    const int row = lane >> 2;
-    const uint8_t* r0 = st + row * 128;
-    const uint8_t* r1 = r0 + 8 * 128;
-    // this lane's chunk of group 0 and 1 of an atom, swizzled
-    const int pos[2] = {((2 * (lane & 3)) ^ row) << 4, ((2 * (lane & 3) + 1) ^ row) << 4};
-    const int first = k0 / 128;
-    for (int j = (warp - first) & (kWarps - 1); j < len / 128; j += kWarps) {
-        if constexpr (!FP8) {
+// This warp's part of one stage: the blocks of 128 whose number (counted over the
+// whole reduction) is the warp's modulo 8, at most one of bf16 and two of 8-bit
+// weights.  Operand A: 16 bytes of row lane / 4 and of row lane / 4 + 8 for each
+// group of products (bf16: 4 of 32 elements, 8-bit: 2 of 64).
+struct StageView {
+    const uint8_t* r0;
+    int pos[2];  // this lane's chunk of group 0 and 1 of an atom, swizzled
+    __device__ __forceinline__ StageView(const uint8_t* st, int lane) {
+        const int row = lane >> 2;
+        r0 = st + row * 128;
+        pos[0] = ((2 * (lane & 3)) ^ row) << 4;
+        pos[1] = ((2 * (lane & 3) + 1) ^ row) << 4;
+    }
+    __device__ __forceinline__ void read(int atom, int g, uint4& lo, uint4& hi) const {
+        const uint8_t* p = r0 + atom * kAtomBytes + pos[g];
+        lo = *reinterpret_cast<const uint4*>(p);
+        hi = *reinterpret_cast<const uint4*>(p + 8 * 128);
+    }
+};
+
+// bf16: the stage is free as soon as the warp's block is in registers, before
+// the products (16 tokens 188.7 -> 184.4 us, 1 token 45.2 -> 44.9).
+struct Block16 {
+    uint4 lo[4], hi[4];
+};
+__device__ __forceinline__ void read_16bit(const StageView& st, int j, Block16& o) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {  // 32 elements each, 2 atoms
-                const int at = (2 * j + (g >> 1)) * kAtomBytes + pos[g & 1];
-                const uint4 lo = *reinterpret_cast<const uint4*>(r0 + at);
-                const uint4 hi = *reinterpret_cast<const uint4*>(r1 + at);
-                const uint4* bp = b + ((first + j) * 4 + g) * NT * 32 + lane;
+    for (int g = 0; g < 4; ++g) st.read(2 * j + (g >> 1), g & 1, o.lo[g], o.hi[g]);
+}
+template <int NT>
+__device__ __forceinline__ void multiply_16bit(const Block16& o, const uint4* b, int block,
+                                               int lane, float (&acc)[NT][4]) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 v = bp[n * 32];
-                    mma16816(acc[n], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
-                    mma16816(acc[n], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
-                }
-            }
-        } else {
-            float part[2][NT][4];  // two chains of products
+    for (int g = 0; g < 4; ++g) {
+        const uint4 lo = o.lo[g], hi = o.hi[g];
+        const uint4* bp = b + (block * 4 + g) * NT * 32 + lane;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const uint4 v = bp[n * 32];
+            mma16816(acc[n], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+            mma16816(acc[n], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+        }
+    }
+}
+
+// 8-bit: one block after the other, straight from the stage (both first, or the
+// stage freed first: 71.5 and 74.4 us at 5 tokens where this takes 71.7).
+template <int NT>
+__device__ __forceinline__ void block_8bit(const StageView& st, const uint4* b,
+                                           const float* scales, int j, int block, bool up,
+                                           int lane, float (&acc)[NT][4]) {
+    float part[2][NT][4];  // two chains of products
 #pragma unroll
-                for (int q = 0; q < 4; ++q) part[0][n][q] = part[1][n][q] = 0.f;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // 64 elements each, 1 atom
-                const int at = j * kAtomBytes + pos[g];
-                const uint4 lo = *reinterpret_cast<const uint4*>(r0 + at);
-                const uint4 hi = *reinterpret_cast<const uint4*>(r1 + at);
-                const uint32_t l4[4] = {lo.x, lo.y, lo.z, lo.w}, h4[4] = {hi.x, hi.y, hi.z, hi.w};
-                const uint4* bp = b + ((first + j) * 2 + g) * 2 * NT * 32 + lane;
+        for (int q = 0; q < 4; ++q) part[0][n][q] = part[1][n][q] = 0.f;
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    uint32_t a[8];
-                    widen(l4[q], a[0], a[2]);
-                    widen(h4[q], a[1], a[3]);
-                    widen(l4[q + 1], a[4], a[6]);
-                    widen(h4[q + 1], a[5], a[7]);
+    for (int g = 0; g < 2; ++g) {
+        uint4 lo, hi;
+        st.read(j, g, lo, hi);
+        const uint32_t l4[4] = {lo.x, lo.y, lo.z, lo.w}, h4[4] = {hi.x, hi.y, hi.z, hi.w};
+        const uint4* bp = b + (block * 2 + g) * 2 * NT * 32 + lane;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 v = bp[((q >> 1) * NT + n) * 32];
-                        mma16816_f16(part[0][n], a[0], a[1], a[2], a[3], v.x, v.y);
-                        mma16816_f16(part[1][n], a[4], a[5], a[6], a[7], v.z, v.w);
-                    }
-                }
-            }
-            const float s0 = scales[j], s1 = up ? scales[16 + j] : s0;
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t a[8];
+            widen(l4[q], a[0], a[2]);
+            widen(h4[q], a[1], a[3]);
+            widen(l4[q + 1], a[4], a[6]);
+            widen(h4[q + 1], a[5], a[7]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(part[0][n][0] + part[1][n][0], s0, acc[n][0]);
-                acc[n][1] = fmaf(part[0][n][1] + part[1][n][1], s0, acc[n][1]);
-                acc[n][2] = fmaf(part[0][n][2] + part[1][n][2], s1, acc[n][2]);
-                acc[n][3] = fmaf(part[0][n][3] + part[1][n][3], s1, acc[n][3]);
+                const uint4 v = bp[((q >> 1) * NT + n) * 32];
+                mma16816_f16(part[0][n], a[0], a[1], a[2], a[3], v.x, v.y);
+                mma16816_f16(part[1][n], a[4], a[5], a[6], a[7], v.z, v.w);
             }
         }
+    }
+    const float s0 = scales[j], s1 = up ? scales[16 + j] : s0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        acc[n][0] = fmaf(part[0][n][0] + part[1][n][0], s0, acc[n][0]);
+        acc[n][1] = fmaf(part[0][n][1] + part[1][n][1], s0, acc[n][1]);
+        acc[n][2] = fmaf(part[0][n][2] + part[1][n][2], s1, acc[n][2]);
+        acc[n][3] = fmaf(part[0][n][3] + part[1][n][3], s1, acc[n][3]);
     }
 }
 
@@ -877,14 +900,23 @@ __device__ __forceinline__ void products(const FewArgs& a, const Smem& s, int wa
                 for (int q = 0; q < 4; ++q) acc[n][q] = 0.f;
         }
         const int k0 = c * p.len;
-        stage_mma<NT, FP8>(s.ring + slot * kStageBytes, s.b, s.scales + slot * 32, k0,
-                           min(p.len, K - k0), up, warp, lane, acc);
+        const StageView st(s.ring + slot * kStageBytes, lane);
+        const int first = k0 / 128, n_blocks = min(p.len, K - k0) / 128;
+        const int j = (warp - first) & (kWarps - 1);
+        Block16 o;
+        if constexpr (FP8) {
+            for (int i = j; i < n_blocks; i += kWarps)
+                block_8bit<NT>(st, s.b, s.scales + slot * 32, i, first + i, up, lane, acc);
+        } else {
+            if (j < n_blocks) read_16bit(st, j, o);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(s.empty + slot);
         if (++slot == a.stages) {
             slot = 0;
             phase ^= 1;
         }
+        if (!FP8 && j < n_blocks) multiply_16bit<NT>(o, s.b, first + j, lane, acc);
         if (c + 1 < p.n) continue;
         if (!hand_over(info, true)) return;
     }
