@@ -21,10 +21,11 @@
 // issuing warps spilled and the kernel took a quarter longer).
 //
 // Many rows (24576 rows in 64 uneven groups, n 2048, k 1536: 128 us, 1.2
-// PFLOP/s): bound by shared memory, 96 bytes a clock written and 96 read per
-// block of 512 clocks, about 870 clocks a block.  A pair of CTAs on one 256-row
-// tile moves two thirds of that, but its accumulators are released across the
-// two SMs, and with the two that TMEM holds it waited for that: 139 us.  Few
+// PFLOP/s): the time does not follow the SM clock (135 us at 1.72 GHz, 130 at
+// about 1.2), it follows what the tiles read from L2: 1.05 GB a launch, 8 TB/s,
+// where the bf16 CTA-pair GEMM reads 9.7.  A pair of CTAs on one 256-row tile
+// reads two thirds of that, but its accumulators are released across the two
+// SMs, and with the two that TMEM holds it waited for that: 139 us.  Few
 // rows (384 rows in 64 groups: 41 us): the weights, at 6.4 TB/s once the first
 // tile has arrived; 4 tiles for some CTAs and 3 for others.
 #include <cudaTypedefs.h>
