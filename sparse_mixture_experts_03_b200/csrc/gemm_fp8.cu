@@ -373,8 +373,9 @@ __global__ void __launch_bounds__(kThreads8, 1) fp8_gemm_kernel(
         int rows = 0, tiles = 0;
         for (int g0 = 0; g0 < a.G; g0 += 32) {
             const int g = g0 + lane;
-            int c = g < a.G ? (a.counts != nullptr ? max(a.counts[g], 0) : a.R) : 0;
-            c = min(c, a.R);  // sums stay below 32 R + R; clamped to 64 bits below
+            // summed as given (64 bits hold 256 of them): a single count beyond R is
+            // seen too; the offsets are cut at R below
+            const int c = g < a.G ? (a.counts != nullptr ? max(a.counts[g], 0) : a.R) : 0;
             long long ir = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
