@@ -33,30 +33,53 @@ import torch
 from . import moe
 
 
+def _weights(name: str, W: torch.Tensor, shape, like: torch.Tensor) -> None:
+    """W is of a type that moe.quantize_weight takes, of this shape, contiguous
+    and on the device of `like`."""
+    moe._dt(W)
+    moe._want(name, W, shape, W.dtype, like)
+
+
 class Fp8MoE:
     """One layer on 8-bit expert weights.
 
-    W_router [E, d] stays as given; W_gate_up [E, 2 inter, d], W_down [E, d,
-    inter] and W_shared (moe.forward's layouts, bfloat16 or float32) are
-    quantised here and not kept.  x is bfloat16, d a multiple of 256.
+    W_router [E, d] (bfloat16) and expert_bias (float32 [E] or None) stay as
+    given; W_gate_up [E, 2 inter, d], W_down [E, d, inter] and W_shared
+    (moe.forward's layouts, bfloat16 or float32) are quantised here and not
+    kept.  x is bfloat16 [T, d] on the weights' device, d a multiple of 256.
+    Other types, shapes and devices are refused (TypeError, ValueError): the
+    library sees only addresses.
     """
 
     def __init__(self, W_router, W_gate_up, W_down, W_shared, k: int, n_group: int,
                  topk_group: int, inter: int, n_shared: int,
                  out_dtype: torch.dtype = torch.float32, gate: str = "sigmoid",
                  expert_bias: Optional[torch.Tensor] = None):
+        if W_router.dim() != 2 or W_router.shape[1] % 256:
+            raise ValueError("W_router must be [E, d] with d a multiple of 256, got "
+                             f"{tuple(W_router.shape)}")
         self.W_router = W_router
-        self.E, self.d = W_router.shape
+        self.E, self.d = E, d = W_router.shape
+        moe._want("W_router", W_router, (E, d), torch.bfloat16, W_router)
+        if expert_bias is not None:
+            moe._want("expert_bias", expert_bias, (E,), torch.float32, W_router)
+        SI = n_shared * inter
+        if (n_shared > 0) != (W_shared is not None):
+            raise ValueError("W_shared is given exactly when there are shared experts")
+        if n_shared:
+            if W_shared.numel() != 3 * SI * d:
+                raise ValueError(f"W_shared must hold {3 * SI * d} values, got {W_shared.numel()}")
+            _weights("W_shared", W_shared, W_shared.shape, W_router)
+        _weights("W_gate_up", W_gate_up, (E, 2 * inter, d), W_router)
+        _weights("W_down", W_down, (E, d, inter), W_router)
         self.k, self.n_group, self.topk_group = k, n_group, topk_group
         self.inter, self.n_shared = inter, n_shared
         self.out_dtype, self.gate, self.expert_bias = out_dtype, gate, expert_bias
-        if (n_shared > 0) != (W_shared is not None):
-            raise ValueError("W_shared is given exactly when there are shared experts")
         self.W_gate_up, self.s_gate_up = moe.quantize_weight(W_gate_up)
         self.W_down, self.s_down = moe.quantize_weight(W_down)
         self.W_shared = self.s_shared = None
         if n_shared:
-            SI, d = n_shared * inter, self.d
+            W_shared = W_shared.view(-1)
             n_gu = 2 * SI * d
             self.W_shared = torch.empty(W_shared.numel(), dtype=moe.E4M3, device=W_shared.device)
             self.s_shared = torch.empty(W_shared.numel() // (128 * 128), dtype=torch.float32,
@@ -87,6 +110,10 @@ class Fp8MoE:
                               counts)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dim() != 2 or x.shape[1] != self.d:
+            raise ValueError(f"x must be [T, {self.d}], got {tuple(x.shape)}")
+        moe._want("x", x, x.shape, torch.bfloat16, self.W_router)
+        moe._on_current("x", x, None)
         T = x.shape[0]
         if T <= self.few:
             return moe.forward_few(x, self.W_router, self.W_gate_up, self.W_down, self.W_shared,
