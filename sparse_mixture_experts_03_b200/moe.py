@@ -495,9 +495,22 @@ def _on_current(name: str, t: torch.Tensor, stream) -> Tuple[int, int]:
                           else stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for work on `stream` (None: the current one).  It comes from that
+    stream's pool: a block of the current stream's pool may still have work
+    queued on it there, which `stream` does not wait for.  The caller may go on
+    to use it on the current stream, so that is recorded."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _used_on(stream, *tensors) -> None:
-    """Tensors allocated here for work on another stream than the current one:
-    their memory is not handed out again before that work is done."""
+    """Tensors used on another stream than the current one: their memory is not
+    handed out again before that work is done."""
     if stream is not None:
         for t in tensors:
             t.record_stream(stream)
@@ -518,13 +531,13 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     px, s = _on_current("x", x, stream)
     R, d = x.shape
     if q is None:
-        q = torch.empty((R, d), dtype=E4M3, device=x.device)
+        q = _empty((R, d), E4M3, x.device, stream)
         pq = q.data_ptr()
     else:
         pq = _want("q", q, (R, d), E4M3, x)
     shape = (_blocks(d), R)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scales = _empty(shape, torch.float32, x.device, stream)
         ps = scales.data_ptr()
     else:
         ps = _want("scales", scales, shape, torch.float32, x)
@@ -549,13 +562,13 @@ def swiglu_quantize_rows(gate_up: torch.Tensor, w: Optional[torch.Tensor] = None
     R, inter = gate_up.shape[0], gate_up.shape[1] // 2
     pw = None if w is None else _want("w", w, (R,), torch.float32, gate_up)
     if q is None:
-        q = torch.empty((R, inter), dtype=E4M3, device=gate_up.device)
+        q = _empty((R, inter), E4M3, gate_up.device, stream)
         pq = q.data_ptr()
     else:
         pq = _want("q", q, (R, inter), E4M3, gate_up)
     shape = (_blocks(inter), R)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=gate_up.device)
+        scales = _empty(shape, torch.float32, gate_up.device, stream)
         ps = scales.data_ptr()
     else:
         ps = _want("scales", scales, shape, torch.float32, gate_up)
@@ -578,13 +591,13 @@ def quantize_weight(W: torch.Tensor, q: Optional[torch.Tensor] = None,
     n, k = W.shape[-2:]
     G = W.shape[0] if W.dim() == 3 else 1
     if q is None:
-        q = torch.empty(W.shape, dtype=E4M3, device=W.device)
+        q = _empty(W.shape, E4M3, W.device, stream)
         pq = q.data_ptr()
     else:
         pq = _want("q", q, W.shape, E4M3, W)
     shape = tuple(W.shape[:-2]) + (_blocks(n), _blocks(k))
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=W.device)
+        scales = _empty(shape, torch.float32, W.device, stream)
         ps = scales.data_ptr()
     else:
         ps = _want("scales", scales, shape, torch.float32, W)
@@ -617,7 +630,7 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     psb = _want("b_scales", b_scales, lead + (_blocks(n), _blocks(k)), torch.float32, a)
     pc = None if counts is None else _want("counts", counts, (G,), torch.int32, a)
     if y is None:
-        y = torch.empty((R, n), dtype=out_dtype, device=a.device)
+        y = _empty((R, n), out_dtype, a.device, stream)
         py = y.data_ptr()
     else:
         py = _want("y", y, (R, n), y.dtype, a)
@@ -680,14 +693,14 @@ def forward_few(x: torch.Tensor, W_router: torch.Tensor, W_gate_up: torch.Tensor
         if scales[2] is not None:
             s_sh = _want("s_shared", scales[2], (sh // (128 * 128),), f32, x)
     if y is None:
-        y = torch.empty((T, d), dtype=out_dtype, device=x.device)
+        y = _empty((T, d), out_dtype, x.device, stream)
     py = _want("y", y, (T, d), y.dtype, x)
     pi = None if topk_idx is None else _want("topk_idx", topk_idx, (T, k), torch.int32, x)
     pw = None if topk_w is None else _want("topk_w", topk_w, (T, k), f32, x)
     pe = None if expert_bias is None else _want("expert_bias", expert_bias, (E,), f32, x)
     if workspace is None:
-        workspace = torch.empty(few_workspace_bytes(T, d, E, k, inter, n_shared),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _empty(few_workspace_bytes(T, d, E, k, inter, n_shared), torch.uint8, x.device,
+                           stream)
     pws = _want("workspace", workspace, workspace.shape, torch.uint8, x)
     st = lib().moe_forward_few(px, pr, pg, pd, psh, s_gu, s_dn, s_sh, T, d, E, k, n_group,
                                topk_group, inter, n_shared, _dt(x), _dt(y), GATES[gate], pe, py,
