@@ -94,38 +94,56 @@ class Fp8MoE:
         # 16 tokens take 164 us in the one call and 145 in steps, 8 tokens 86 and 113
         self.few = min(8, moe.few_max_tokens(self.d, self.E, k, inter, n_shared))
 
-    def shared(self, x: torch.Tensor) -> Optional[torch.Tensor]:
+    def workspace_bytes(self, T: int) -> int:
+        """A workspace for any batch of up to T tokens."""
+        few = min(T, self.few)
+        return max(moe.lib().moe_dispatch_workspace_bytes(T, self.E, self.k), 256,
+                   moe.few_workspace_bytes(few, self.d, self.E, self.k, self.inter,
+                                           self.n_shared) if few else 0)
+
+    def shared(self, x: torch.Tensor,
+               status_ws: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
         """The shared experts' sum, fp32 [T, d] (None without shared experts)."""
         if not self.n_shared:
             return None
-        gate_up = moe.matmul_fp8(*moe.quantize_rows(x), *self.shared_gate_up)
+        gate_up = moe.matmul_fp8(*moe.quantize_rows(x), *self.shared_gate_up, status_ws=status_ws)
         return moe.matmul_fp8(*moe.swiglu_quantize_rows(gate_up), *self.shared_down,
-                              out_dtype=torch.float32)
+                              out_dtype=torch.float32, status_ws=status_ws)
 
-    def experts(self, rows: torch.Tensor, w: torch.Tensor, counts: torch.Tensor) -> torch.Tensor:
+    def experts(self, rows: torch.Tensor, w: torch.Tensor, counts: torch.Tensor,
+                status_ws: Optional[torch.Tensor] = None) -> torch.Tensor:
         """w[r] * expert of row r, bfloat16; rows in expert order, counts[e] of
-        expert e."""
-        gate_up = moe.matmul_fp8(*moe.quantize_rows(rows), self.W_gate_up, self.s_gate_up, counts)
+        expert e.  status_ws as moe.matmul_fp8's."""
+        gate_up = moe.matmul_fp8(*moe.quantize_rows(rows), self.W_gate_up, self.s_gate_up, counts,
+                                 status_ws=status_ws)
         return moe.matmul_fp8(*moe.swiglu_quantize_rows(gate_up, w), self.W_down, self.s_down,
-                              counts)
+                              counts, status_ws=status_ws)
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y [T, d].  workspace: uint8, workspace_bytes(T), 256-byte aligned;
+        moe.device_status(workspace) then gives the first device error of the
+        call's steps, if any (without tokens nothing is queued and it stays as
+        it was).  Calls that overlap in time need workspaces of their own."""
         if x.dim() != 2 or x.shape[1] != self.d:
             raise ValueError(f"x must be [T, {self.d}], got {tuple(x.shape)}")
         moe._want("x", x, x.shape, torch.bfloat16, self.W_router)
         moe._on_current("x", x, None)
         T = x.shape[0]
+        if workspace is not None:
+            moe._want("workspace", workspace, workspace.shape, torch.uint8, x)
         if T <= self.few:
             return moe.forward_few(x, self.W_router, self.W_gate_up, self.W_down, self.W_shared,
                                    self.k, self.n_group, self.topk_group, self.inter,
                                    self.n_shared, scales=(self.s_gate_up, self.s_down,
                                                           self.s_shared),
                                    out_dtype=self.out_dtype, gate=self.gate,
-                                   expert_bias=self.expert_bias)
+                                   expert_bias=self.expert_bias, workspace=workspace)
+        # dispatch clears the workspace's status words, the other steps set them
         disp = moe.dispatch(x, self.W_router, self.k, self.n_group, self.topk_group,
-                            gate=self.gate, expert_bias=self.expert_bias)
-        y_shared = self.shared(x)
-        rows = self.experts(disp.x_perm, disp.w_perm, disp.counts)
-        return moe.combine(rows, disp.slot_row, y_shared, T, self.k, self.out_dtype)
+                            gate=self.gate, expert_bias=self.expert_bias, workspace=workspace)
+        y_shared = self.shared(x, workspace)
+        rows = self.experts(disp.x_perm, disp.w_perm, disp.counts, workspace)
+        return moe.combine(rows, disp.slot_row, y_shared, T, self.k, self.out_dtype,
+                           status_ws=workspace)
 
     __call__ = forward

@@ -90,3 +90,47 @@ def test_tokens_are_checked_before_a_path_is_chosen(quantised, make, error, T):
     layer = fp8.Fp8MoE(**weights())
     with pytest.raises(error):
         layer(make(T))
+
+
+def test_every_step_is_given_the_workspace(quantised, monkeypatch):
+    """Dispatch first, which clears the status words; then the steps that set them."""
+    seen = []
+
+    def take(name, key, out):
+        def call(*args, **kw):
+            seen.append((name, kw.get(key)))
+            return out
+        monkeypatch.setattr(moe, name, call)
+    t = torch.zeros(1)
+    take("dispatch", "workspace", moe.Dispatched(t, t, t, t, t, t))
+    take("matmul_fp8", "status_ws", t)
+    take("combine", "status_ws", t)
+    take("forward_few", "workspace", t)
+    for name in ("quantize_rows", "swiglu_quantize_rows"):
+        monkeypatch.setattr(moe, name, lambda *a, **kw: (t, t))
+    monkeypatch.setattr(moe, "_on_current", lambda *a: (0, 0))
+    layer = fp8.Fp8MoE(**weights())
+    ws = torch.zeros(layer.workspace_bytes(40), dtype=torch.uint8)
+    layer(torch.zeros(40, D, dtype=BF), ws)
+    assert [n for n, _ in seen] == ["dispatch"] + 4 * ["matmul_fp8"] + ["combine"]
+    assert all(w is ws for _, w in seen)
+    seen.clear()
+    layer(torch.zeros(4, D, dtype=BF), workspace=ws)
+    assert seen == [("forward_few", ws)]
+    for bad in (ws.int(), ws[::2], ws.to("meta")):
+        with pytest.raises((TypeError, ValueError)):
+            layer(torch.zeros(40, D, dtype=BF), bad)
+
+
+@pytest.mark.parametrize("inter", [I, 192])  # with the one call, and without
+def test_workspace_of_a_batch_holds_smaller_ones(quantised, inter):
+    w = weights(W_gate_up=torch.zeros(E, 2 * inter, D, dtype=BF), inter=inter,
+                W_down=torch.zeros(E, D, inter, dtype=BF),
+                W_shared=torch.zeros(3 * S * inter * D, dtype=BF))
+    layer = fp8.Fp8MoE(**w)
+    sizes = [layer.workspace_bytes(T) for T in range(200)]
+    assert sizes == sorted(sizes) and sizes[0] >= 256
+    for T in range(1, 200):
+        need = (moe.few_workspace_bytes(T, D, E, K, inter, S) if T <= layer.few
+                else moe.lib().moe_dispatch_workspace_bytes(T, E, K))
+        assert sizes[T] >= need

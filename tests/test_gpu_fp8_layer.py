@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from sparse_mixture_experts_03_b200 import moe
 from sparse_mixture_experts_03_b200.fp8 import Fp8MoE
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +40,68 @@ def test_wrong_types_and_shapes_are_refused_at_every_batch_size():
             with pytest.raises(error):
                 layer(x)
         assert layer(randn(T, D)).shape == (T, D)
+
+
+def test_status_of_a_call():
+    layer = make()
+    ws = torch.full((layer.workspace_bytes(1100),), 0xAB, dtype=torch.uint8, device=DEV)
+    for T in (1, 8, 9, 300, 1100, 5):  # whatever the last batch left in the workspace
+        x = randn(T, D, seed=T)
+        y = layer(x, workspace=ws)
+        assert moe.device_status(ws)[0] == moe.MOE_OK
+        assert torch.equal(y, layer(x))
+
+
+def test_a_steps_error_is_seen(monkeypatch):
+    layer, x = make(), randn(40, D)
+    ws = torch.zeros(layer.workspace_bytes(40), dtype=torch.uint8, device=DEV)
+    disp = moe.dispatch(x, layer.W_router, K, G, TG)
+    status = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    layer.experts(disp.x_perm, disp.w_perm, disp.counts, status)
+    assert moe.device_status(status)[0] == moe.MOE_OK
+    layer.experts(disp.x_perm, disp.w_perm, disp.counts + 1, status)
+    assert moe.device_status(status)[0] == moe.MOE_ERR_DEVICE
+
+    dispatch = moe.dispatch
+
+    def too_many(*args, **kw):  # the rows that there are still go to some expert
+        out = dispatch(*args, **kw)
+        out.counts[0] += 40 * K
+        return out
+    good = layer(x, workspace=ws)
+    monkeypatch.setattr(moe, "dispatch", too_many)
+    layer(x, workspace=ws)
+    assert moe.device_status(ws)[0] == moe.MOE_ERR_DEVICE
+    monkeypatch.setattr(moe, "dispatch", dispatch)
+    assert torch.equal(layer(x, workspace=ws), good)  # and the next call starts anew
+    assert moe.device_status(ws)[0] == moe.MOE_OK
+
+
+def test_workspaces_that_do_not_fit_are_refused():
+    layer = make()
+    for T in (4, 40):
+        x = randn(T, D)
+        with pytest.raises(moe.MoeError):
+            layer(x, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+        with pytest.raises(moe.MoeError):  # not aligned
+            layer(x, workspace=torch.empty(1 << 22, dtype=torch.uint8, device=DEV)[16:])
+        with pytest.raises(ValueError):
+            layer(x, workspace=torch.empty(1 << 22, dtype=torch.uint8))
+
+
+def test_a_captured_call_with_its_workspace():
+    layer = make()
+    for T in (5, 40):
+        x = randn(T, D, seed=T)
+        ws = torch.empty(layer.workspace_bytes(T), dtype=torch.uint8, device=DEV)
+        layer(x, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = layer(x, ws)
+        for seed in (1, 2):
+            x.copy_(randn(T, D, seed=seed))
+            g.replay()
+            assert torch.equal(y, layer(x))
+            assert moe.device_status(ws)[0] == moe.MOE_OK
+        del g
