@@ -46,7 +46,8 @@ class Fp8MoE:
     W_router [E, d] (bfloat16) and expert_bias (float32 [E] or None) stay as
     given; W_gate_up [E, 2 inter, d], W_down [E, d, inter] and W_shared
     (moe.forward's layouts, bfloat16 or float32) are quantised here and not
-    kept.  x is bfloat16 [T, d] on the weights' device, d a multiple of 256.
+    kept.  x is bfloat16 [T, d] on the weights' device, d a multiple of 256,
+    inter of 16.
     Other types, shapes and devices are refused (TypeError, ValueError): the
     library sees only addresses.
     """
@@ -82,13 +83,13 @@ class Fp8MoE:
             W_shared = W_shared.view(-1)
             n_gu = 2 * SI * d
             self.W_shared = torch.empty(W_shared.numel(), dtype=moe.E4M3, device=W_shared.device)
-            self.s_shared = torch.empty(W_shared.numel() // (128 * 128), dtype=torch.float32,
+            s_gu, s_dn = (moe._blocks(2 * SI), d // 128), (d // 128, moe._blocks(SI))
+            n_s = s_gu[0] * s_gu[1]
+            self.s_shared = torch.empty(n_s + s_dn[0] * s_dn[1], dtype=torch.float32,
                                         device=W_shared.device)
-            n_s = n_gu // (128 * 128)
             self.shared_gate_up = (self.W_shared[:n_gu].view(2 * SI, d),
-                                   self.s_shared[:n_s].view(2 * SI // 128, d // 128))
-            self.shared_down = (self.W_shared[n_gu:].view(d, SI),
-                                self.s_shared[n_s:].view(d // 128, SI // 128))
+                                   self.s_shared[:n_s].view(s_gu))
+            self.shared_down = (self.W_shared[n_gu:].view(d, SI), self.s_shared[n_s:].view(s_dn))
             moe.quantize_weight(W_shared[:n_gu].view(2 * SI, d), *self.shared_gate_up)
             moe.quantize_weight(W_shared[n_gu:].view(d, SI), *self.shared_down)
         # 16 tokens take 164 us in the one call and 145 in steps, 8 tokens 86 and 113

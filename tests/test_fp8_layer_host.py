@@ -134,3 +134,19 @@ def test_workspace_of_a_batch_holds_smaller_ones(quantised, inter):
         need = (moe.few_workspace_bytes(T, D, E, K, inter, S) if T <= layer.few
                 else moe.lib().moe_dispatch_workspace_bytes(T, E, K))
         assert sizes[T] >= need
+
+
+@pytest.mark.parametrize("inter,n_shared", [(192, 1), (16, 1), (80, 3), (48, 2), (128, 1)])
+def test_shared_experts_of_any_size_that_routed_ones_may_have(quantised, inter, n_shared):
+    SI = n_shared * inter
+    layer = fp8.Fp8MoE(**weights(inter=inter, n_shared=n_shared,
+                                 W_gate_up=torch.zeros(E, 2 * inter, D, dtype=BF),
+                                 W_down=torch.zeros(E, D, inter, dtype=BF),
+                                 W_shared=torch.zeros(3 * SI * D, dtype=BF)))
+    up, s_up = layer.shared_gate_up
+    down, s_down = layer.shared_down
+    assert up.shape == (2 * SI, D) and s_up.shape == (-(-2 * SI // 128), D // 128)
+    assert down.shape == (D, SI) and s_down.shape == (D // 128, -(-SI // 128))
+    assert up.data_ptr() == layer.W_shared.data_ptr()
+    assert s_up.data_ptr() == layer.s_shared.data_ptr()
+    assert s_down.data_ptr() == s_up.data_ptr() + 4 * s_up.numel()
