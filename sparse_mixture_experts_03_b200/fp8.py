@@ -132,6 +132,8 @@ class Fp8MoE:
         T = x.shape[0]
         if workspace is not None:
             moe._want("workspace", workspace, workspace.shape, torch.uint8, x)
+        if T == 0:
+            return torch.empty((0, self.d), dtype=self.out_dtype, device=x.device)
         if T <= self.few:
             return moe.forward_few(x, self.W_router, self.W_gate_up, self.W_down, self.W_shared,
                                    self.k, self.n_group, self.topk_group, self.inter,

@@ -150,3 +150,14 @@ def test_shared_experts_of_any_size_that_routed_ones_may_have(quantised, inter, 
     assert up.data_ptr() == layer.W_shared.data_ptr()
     assert s_up.data_ptr() == layer.s_shared.data_ptr()
     assert s_down.data_ptr() == s_up.data_ptr() + 4 * s_up.numel()
+
+
+@pytest.mark.parametrize("inter", [I, 192])  # with the one call, and without
+@pytest.mark.parametrize("out", [F32, BF])
+def test_no_tokens(quantised, monkeypatch, inter, out):
+    monkeypatch.setattr(moe, "_on_current", lambda *a: (0, 0))
+    layer = fp8.Fp8MoE(**weights(inter=inter, W_gate_up=torch.zeros(E, 2 * inter, D, dtype=BF),
+                                 W_down=torch.zeros(E, D, inter, dtype=BF), out_dtype=out,
+                                 W_shared=torch.zeros(3 * S * inter * D, dtype=BF)))
+    y = layer(torch.zeros(0, D, dtype=BF))
+    assert y.shape == (0, D) and y.dtype == out

@@ -145,3 +145,12 @@ def check_tokens(layer, x):
 @pytest.mark.parametrize("inter,n_shared", [(192, 1), (80, 3), (208, 2), (64, 0), (256, 2)])
 def test_every_token_at_odd_expert_sizes(inter, n_shared, T):
     check_tokens(make(S=n_shared, I=inter, seed=T), randn(T, D, seed=T + 9))
+
+
+@pytest.mark.parametrize("inter", [192, 256])  # without the one call, and with it
+def test_no_tokens(inter):
+    layer = make(I=inter, S=1)
+    assert (layer.few == 0) == (inter == 192)
+    for ws in (None, torch.zeros(layer.workspace_bytes(0), dtype=torch.uint8, device=DEV)):
+        y = layer(randn(0, D), ws)
+        assert y.shape == (0, D) and y.dtype == torch.float32
