@@ -517,7 +517,8 @@ MOE_API int moe_quantize_weight(const void *W, int G, int n, int k, int in_dt, v
  *   status_ws device workspace (256 bytes, 256-byte aligned) whose status
  *             word receives MOE_ERR_DEVICE or MOE_ERR_TIMEOUT, or NULL.  It is
  *             not reset by the call (moe_clear_device_status does)
- * Limits: 1 <= G <= 256.  R = 0 queues nothing.
+ * Limits: 1 <= G <= 256; R and k at most 2^31 - 128, n at most 2^31 - 256
+ * (else MOE_ERR_UNSUPPORTED).  R = 0 queues nothing.
  */
 MOE_API int moe_matmul_fp8(const void *a, const float *a_scales, const void *b,
                            const float *b_scales, const int32_t *counts, int R, int G, int n,

@@ -669,6 +669,8 @@ MOE_API int moe_matmul_fp8(const void* a, const float* a_scales, const void* b,
     if (counts == nullptr && G != 1) return MOE_ERR_INVALID_ARG;
     // tiles are numbered in 32 bits, with room for a step behind the last
     const long long m_tiles = ((long long)R + kM8 - 1) / kM8 + G;
+    // rows and depth are rounded up to blocks of 128, columns to 256, in 32 bits
+    if (R > INT_MAX - 127 || k > INT_MAX - 127 || n > INT_MAX - 255) return MOE_ERR_UNSUPPORTED;
     if (k % 16 != 0 || m_tiles * (((long long)n + 63) / 64) > (1LL << 30))
         return MOE_ERR_UNSUPPORTED;
     if (R == 0) return MOE_OK;
