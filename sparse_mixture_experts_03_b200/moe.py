@@ -495,6 +495,12 @@ def _on_current(name: str, t: torch.Tensor, stream) -> Tuple[int, int]:
                           else stream.cuda_stream)
 
 
+def _sizes(*sizes: int) -> None:
+    """The library takes sizes as C ints, and ctypes cuts larger ones without a word."""
+    if max(sizes) >= 2 ** 31:
+        raise ValueError(f"sizes must be below 2^31, got {max(sizes)}")
+
+
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """Memory for work on `stream` (None: the current one).  It comes from that
     stream's pool: a block of the current stream's pool may still have work
@@ -530,6 +536,7 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
         raise ValueError(f"x must be [R, d], got {tuple(x.shape)}")
     px, s = _on_current("x", x, stream)
     R, d = x.shape
+    _sizes(R, d)
     if q is None:
         q = _empty((R, d), E4M3, x.device, stream)
         pq = q.data_ptr()
@@ -560,6 +567,7 @@ def swiglu_quantize_rows(gate_up: torch.Tensor, w: Optional[torch.Tensor] = None
         raise ValueError(f"gate_up must be [R, 2*inter], got {tuple(gate_up.shape)}")
     px, s = _on_current("gate_up", gate_up, stream)
     R, inter = gate_up.shape[0], gate_up.shape[1] // 2
+    _sizes(R, inter)
     pw = None if w is None else _want("w", w, (R,), torch.float32, gate_up)
     if q is None:
         q = _empty((R, inter), E4M3, gate_up.device, stream)
@@ -590,6 +598,7 @@ def quantize_weight(W: torch.Tensor, q: Optional[torch.Tensor] = None,
     px, s = _on_current("W", W, stream)
     n, k = W.shape[-2:]
     G = W.shape[0] if W.dim() == 3 else 1
+    _sizes(G, n, k)
     if q is None:
         q = _empty(W.shape, E4M3, W.device, stream)
         pq = q.data_ptr()
@@ -625,6 +634,7 @@ def matmul_fp8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scale
     lead = tuple(b.shape[:-2])
     n = b.shape[-2]
     G = lead[0] if lead else 1
+    _sizes(R, G, n, k)
     psa = _want("a_scales", a_scales, (_blocks(k), R), torch.float32, a)
     pb = _want("b", b, lead + (n, k), E4M3, a)
     psb = _want("b_scales", b_scales, lead + (_blocks(n), _blocks(k)), torch.float32, a)

@@ -3,6 +3,7 @@ queued)."""
 import ctypes
 
 import pytest
+import torch
 
 from sparse_mixture_experts_03_b200 import moe
 
@@ -29,3 +30,30 @@ def test_sizes_whose_tiles_pass_31_bits_are_refused(sizes):
                                    dict(R=1, n=INT_MAX - 255, k=16)])
 def test_the_largest_sizes_are_taken(sizes):
     assert product(**sizes) == BAD  # the missing pointers, checked after the sizes
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda n: moe.quantize_rows(meta(n, 16)),
+    lambda n: moe.swiglu_quantize_rows(meta(n, 32)),
+    lambda n: moe.quantize_weight(meta(n, 16)),
+    lambda n: moe.quantize_weight(meta(n, 1, 16)),
+    lambda n: moe.quantize_weight(meta(1, n)),
+    lambda n: moe.matmul_fp8(meta(n, 16, dtype=moe.E4M3), meta(1, n, dtype=torch.float32),
+                             meta(1, 16, dtype=moe.E4M3), meta(1, 1, dtype=torch.float32)),
+    lambda n: moe.matmul_fp8(meta(1, 16, dtype=moe.E4M3), meta(1, 1, dtype=torch.float32),
+                             meta(n, 16, dtype=moe.E4M3),
+                             meta((n + 127) // 128, 1, dtype=torch.float32)),
+])
+def test_sizes_beyond_a_c_int_are_refused(monkeypatch, call):
+    """2^32 + 16 rows are not 16 rows."""
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: pytest.fail(f"{name} was reached with {args}")
+    monkeypatch.setattr(moe, "lib", lambda: Library())
+    monkeypatch.setattr(moe, "_on_current", lambda name, t, s: (0, 0))
+    for n in (2 ** 31, 2 ** 32 + 16):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(n)
