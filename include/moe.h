@@ -479,7 +479,8 @@ MOE_API int moe_quantize_rows(const void *x, int R, int d, int in_dt, void *q, f
 
 /*
  * moe_swiglu_quantize_rows -- h = silu(gate) * up of each row (computed in
- * fp32), in 8 bits.
+ * fp32, to within 2^-22 (4 + |gate|) of itself; zero for gates below -88.7,
+ * where fp32's exponential ends), in 8 bits.
  *   gate_up  device, bf16 [R, 2*inter]: gate, then up; inter % 16 == 0
  *   w        device, f32 [R], or NULL: each row's scales are multiplied by
  *            w[r] (a gate weight: the product of the row is w[r] times larger)
@@ -503,7 +504,8 @@ MOE_API int moe_quantize_weight(const void *W, int G, int n, int k, int in_dt, v
  *   y[r, n] = sum_j a_scales[j, r] b_scales[g, n / 128, j] *
  *             sum_{k in block j} a[r, k] b[g, n, k]
  * The sum inside a block is the tensor core's, the sum over blocks fp32, y is
- * rounded once.
+ * rounded once.  The product of the two scales is taken first, as an fp32
+ * number: it has to lie in fp32's range.
  *   a         device, e4m3 [R, k], k % 16 == 0
  *   a_scales  device, f32 [ceil(k / 128), R]
  *   b         device, e4m3 [G, n, k]
@@ -546,7 +548,7 @@ MOE_API size_t moe_few_workspace_bytes(int T, int d, int E, int k, int inter, in
  * h is rounded once to bf16, all sums are fp32 and y is rounded once: the
  * experts' outputs are not rounded on their own as in moe_forward.  Sums run
  * in a fixed order: results are bitwise reproducible.  Other arguments as
- * moe_forward_ex.  Limits: d % 256 == 0, inter % 128 == 0, n_shared <= 64,
+ * moe_forward_ex, except that there is no expert_load output.  Limits: d % 256 == 0, inter % 128 == 0, n_shared <= 64,
  * T <= moe_few_max_tokens(...) (else MOE_ERR_UNSUPPORTED).  The workspace
  * needs no initialisation; its first 256 bytes are the status word
  * (moe_get_device_status).  Calls that overlap in time need workspaces of

@@ -18,12 +18,14 @@
 // sub-partition: TMEM lanes 32 (w % 4).., columns half (w - 4) / 4).  128 sums a
 // thread need more registers than an even split leaves: warps 0..3 hand some of
 // theirs over (of the launch's 384 x 168, 128 x 120 + 256 x 192; with 128 x 56 the
-// issuing warps spilled and the kernel took a quarter longer).
+// issuing warps spilled and the kernel took a quarter longer).  At 256 columns 24
+// bytes a thread still spill (48 bytes of stores, 176 of loads in the code), at
+// the other widths none.
 //
 // Many rows (24576 rows in 64 uneven groups, n 2048, k 1536: 128 us, 1.2
-// PFLOP/s): the time does not follow the SM clock (135 us at 1.72 GHz, 130 at
-// about 1.2), it follows what the tiles read from L2: 1.05 GB a launch, 8 TB/s,
-// where the bf16 CTA-pair GEMM reads 9.7.  A pair of CTAs on one 256-row tile
+// PFLOP/s, in bursts of up to 40 ms; in a longer loop, under the power cap at
+// 1.57 GHz, 155 us): the time goes with what the tiles read from L2, 1.05 GB a
+// launch, 8 TB/s, where the bf16 CTA-pair GEMM reads 9.7.  A pair of CTAs on one 256-row tile
 // reads two thirds of that, but its accumulators are released across the two
 // SMs, and with the two that TMEM holds it waited for that: 139 us.  Few
 // rows (384 rows in 64 groups: 41 us): the weights, at 6.4 TB/s once the first

@@ -39,8 +39,10 @@ __device__ __forceinline__ void set_status(int* status, int code, int where, int
 // writes are visible (no-op for a kernel launched without programmatic
 // dependent launch).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// This CTA's work that later kernels depend on is done: the next kernel may be
-// scheduled once every CTA of this grid has signalled or exited.
+// The next kernel of the stream may be scheduled once every CTA of this grid has
+// signalled or exited.  That says nothing about this grid's writes: whoever reads
+// them waits for its completion with pdl_wait, so a kernel may signal as early as
+// its own pdl_wait has returned.
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

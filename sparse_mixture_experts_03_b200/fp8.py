@@ -3,7 +3,10 @@
 The layer of moe.forward for serving, at half the weight bytes: the router
 stays as it is, the experts' weights are quantised once when the layer is made.
 Up to 8 tokens the layer is one call (moe.forward_few, whose activations stay
-16-bit); above that it is
+16-bit: a token's result is within 1.8e-3 of 64 bits on the same 8-bit weights,
+as a norm); above that it is the following steps, whose activations are 8-bit
+(4.4e-2 on the same weights).  Against the layer on 16-bit weights the two are
+4.7e-2 and 6.4e-2 off: a token's result depends on the size of its batch.
 
   1. dispatch   route and copy each chosen (token, expert) row into expert order
   2. quantise   rows to 8 bits, one scale per 128 columns
@@ -17,7 +20,7 @@ with steps 2-5 once more for the shared experts, on all tokens.
 What it is for: half the memory, and decode.  At d 2048, inter 1536, 64 + 4
 experts it takes 36 us at 1 token, 86 at 8, 171 at 64 and 294 at 1024, where
 moe.forward on 16-bit weights takes 80, 144, 228 and 326.  A prefill of 4096
-tokens is slower, 770 to 910 us against 740: the 8-bit product with arbitrary
+tokens is slower, 750 to 800 us against 730: the 8-bit product with arbitrary
 fp32 scales runs no faster than the 16-bit one (its sums leave the tensor core
 every 128 columns), and the rows have to be made 8-bit.
 
@@ -92,7 +95,9 @@ class Fp8MoE:
             self.shared_down = (self.W_shared[n_gu:].view(d, SI), self.s_shared[n_s:].view(s_dn))
             moe.quantize_weight(W_shared[:n_gu].view(2 * SI, d), *self.shared_gate_up)
             moe.quantize_weight(W_shared[n_gu:].view(d, SI), *self.shared_down)
-        # 16 tokens take 164 us in the one call and 145 in steps, 8 tokens 86 and 113
+        # 16 tokens take 164 us in the one call and 145 in steps, 8 tokens 86 and 113:
+        # measured on one layer, that of the docstring above; `few` may be set lower
+        # (0: always the steps) where another layer's figures cross elsewhere
         self.few = min(8, moe.few_max_tokens(self.d, self.E, k, inter, n_shared))
 
     def workspace_bytes(self, T: int) -> int:
